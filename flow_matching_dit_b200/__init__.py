@@ -10,6 +10,10 @@ package only marshals arguments.  PyTorch supplies device memory and streams.
 ``geom`` is any object with the fields of ``gdit_config`` (for example
 ``synth.Geometry``); ``weights`` maps the names of ``include/gdit.h`` to numpy
 arrays (float32, or uint16 holding bf16 bit patterns).
+
+``linear``, ``norm_residual`` and ``attention`` are the operators of a
+transformer block over packed tokens, for the layers a program runs around the
+head; ``op_status`` reports what they found wrong on the device (see ``ops``).
 """
 
 from __future__ import annotations
@@ -26,7 +30,17 @@ from ._lib import (GDIT_BF16, GDIT_F32, GDIT_FLAG_NO_GRAPH, GDIT_FLAG_NO_PAIR, G
 from .build import build  # noqa: F401
 
 __all__ = ["ActionHead", "GditError", "lib", "build", "check_io_shapes", "is_checked", "GDIT_BF16", "GDIT_F32",
-           "GDIT_FLAG_NO_GRAPH", "GDIT_FLAG_NO_SMALL", "GDIT_FLAG_STRICT_PROFILES"]
+           "GDIT_FLAG_NO_GRAPH", "GDIT_FLAG_NO_SMALL", "GDIT_FLAG_STRICT_PROFILES",
+           "linear", "norm_residual", "attention", "op_status"]
+
+
+def __getattr__(name):
+    # the operators, on first use: .ops imports torch, which the rest of the binding needs only in its calls
+    if name in ("linear", "norm_residual", "attention", "op_status"):
+        from . import ops
+        globals()[name] = f = getattr(ops, name)
+        return f
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def is_checked() -> bool:

@@ -31,6 +31,14 @@ GDIT_FLAG_NO_SMALL = 4
 GDIT_FLAG_NO_TMA_STORE = 8
 GDIT_FLAG_NO_PAIR = 16
 GDIT_FLAG_NO_SKINNY = 32
+GDIT_ACT_NONE = 0
+GDIT_ACT_RELU = 1
+GDIT_ACT_GELU = 2
+GDIT_ACT_GELU_TANH = 3
+GDIT_ACT_SILU = 4
+GDIT_NORM_NONE = 0
+GDIT_NORM_LAYER = 1
+GDIT_NORM_RMS = 2
 
 
 class gdit_config(ctypes.Structure):
@@ -54,6 +62,31 @@ class gdit_kernel_stat(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+
+
+class gdit_linear_args(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("x", "w", "bias", "residual", "out")] + \
+        [(n, _L) for n in ("m", "ldx", "ldw", "ldr", "ldo")] + [(n, _I) for n in ("n", "k", "out_dtype", "activation")]
+
+
+class gdit_norm_args(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("h", "y", "out_h", "out_u", "post_gain", "post_bias", "gate", "pre_gain", "pre_bias",
+                                  "scale", "shift", "row_group")] + \
+        [(n, _L) for n in ("rows", "ldh", "ldy", "ldoh", "ldou")] + \
+        [(n, _I) for n in ("dim", "h_dtype", "y_dtype", "u_dtype", "post", "pre", "gate_groups", "mod_groups")] + \
+        [("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class gdit_attention_args(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("q", "k", "v", "out", "lse", "cu_q", "cu_k", "k_len")] + \
+        [(n, _L) for n in ("total_q", "total_k", "q_token_stride", "q_head_stride", "k_token_stride",
+                           "k_head_stride", "v_token_stride", "v_head_stride", "out_token_stride",
+                           "out_head_stride")] + \
+        [(n, _I) for n in ("batch", "heads", "kv_heads", "head_dim", "max_q", "max_k", "causal")] + \
+        [("scale", ctypes.c_float)]
+
+
 _SIGS = {
     "gdit_create": (_I, [ctypes.POINTER(gdit_config), ctypes.POINTER(gdit_tensor), _I, ctypes.POINTER(_P)]),
     "gdit_destroy": (None, [_P]),
@@ -77,6 +110,10 @@ _SIGS = {
     "gdit_is_checked": (_I, []),
     "gdit_check_canaries": (_I, [_P, ctypes.POINTER(ctypes.c_longlong)]),
     "gdit_debug_poke_guard": (_I, [_P, _I]),
+    "gdit_linear": (_I, [ctypes.POINTER(gdit_linear_args), _P]),
+    "gdit_norm_residual": (_I, [ctypes.POINTER(gdit_norm_args), _P]),
+    "gdit_attention": (_I, [ctypes.POINTER(gdit_attention_args), _P]),
+    "gdit_op_status": (_I, [_I, _P]),
 }
 
 _lock = threading.Lock()
@@ -205,3 +242,19 @@ def gdit_check_canaries(h, out):
 
 def gdit_debug_poke_guard(h, which):
     return lib().gdit_debug_poke_guard(h, which)
+
+
+def gdit_linear(args, stream):
+    return lib().gdit_linear(args, stream)
+
+
+def gdit_norm_residual(args, stream):
+    return lib().gdit_norm_residual(args, stream)
+
+
+def gdit_attention(args, stream):
+    return lib().gdit_attention(args, stream)
+
+
+def gdit_op_status(device, stream):
+    return lib().gdit_op_status(device, stream)

@@ -1,7 +1,7 @@
 """In-tree build of the CUDA library ``libgdit.so`` for sm_100a.
 
 ``python -m flow_matching_dit_b200.build`` (or ``build()``) compiles
-``csrc/gdit.cu`` with nvcc into ``flow_matching_dit_b200/libgdit.so``, and
+``csrc/gdit.cu`` (the action head) and ``csrc/ops.cu`` (the operators) with nvcc into ``flow_matching_dit_b200/libgdit.so``, and
 with ``checked=True`` into ``libgdit_checked.so``, the range-checked build
 (``-DGDIT_CHECKED=1``: guard bands around device allocations, index checks in
 the kernels).  nvcc cross-compiles, so this works on a machine without a GPU.
@@ -34,7 +34,7 @@ def command(out: str = LIB, checked: bool = False) -> list:
     return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
             "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"),
             "-diag-suppress", "177"] + (["-DGDIT_CHECKED=1"] if checked else []) + \
-        ["-o", out, os.path.join(PKG, "csrc", "gdit.cu")]
+        ["--threads", "2", "-o", out, os.path.join(PKG, "csrc", "gdit.cu"), os.path.join(PKG, "csrc", "ops.cu")]
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -343,6 +343,162 @@ int gdit_test_gemm(const void* A, const void* B, const float* bias, float* C,
 int gdit_gemm_static_scratch(const void* A, const void* B, const float* bias, float* C,
                              int M, int N, int K, int bn, int splits, void* cuda_stream);
 
+/* --------------------------------------------------------------- operators
+ * The operators of a transformer block over packed tokens, for the layers that
+ * a program runs around the action head (the ones whose output are its
+ * backbone_features, or layers between the two):
+ *   gdit_linear         out = act(x W^T + bias) + residual
+ *   gdit_norm_residual  h' = a h + gate * post(y), u = pre(h') (1 + scale) + shift
+ *   gdit_attention      softmax(scale q k^T) v over packed sequences
+ * (Isaac-GR00T architecture page, "Transformer block structure": norm,
+ * attention and feed-forward, each added to the residual stream.)
+ *
+ * Common rules
+ *   - No handle, no allocation, no workspace, no synchronization: a call
+ *     validates its arguments on the host and enqueues one kernel on
+ *     cuda_stream.  Calls are independent of one another: they may run at the
+ *     same time from several host threads and streams, and may be captured in
+ *     CUDA graphs (no set-up call is needed before a capture).
+ *   - Device pointers belong to the calling thread's current device, the
+ *     stream too.  Matrices are row-major with the row strides given, in
+ *     elements; the innermost dimension is dense.
+ *   - Zero rows (m, rows, total_q or batch 0) is a valid call that does nothing.
+ *   - Sums, softmax statistics and norms are f32; outputs are rounded once,
+ *     to nearest even.
+ *   - Results are the same bit for bit from call to call on the same inputs.
+ *   - What the host cannot see is checked on the device: a row_group entry out
+ *     of range, sequence offsets that decrease, end past the tensor or exceed
+ *     max_q / max_k.  Nothing is read or written outside the tensors for them;
+ *     the call's affected rows are NaN (row_group) or left as they were
+ *     (attention), and gdit_op_status reports GDIT_EDEVICE.
+ *   - Every call returns GDIT_OK, GDIT_EINVAL, GDIT_ECUDA or GDIT_ENODEV; the
+ *     detail message is gdit_last_error(NULL) on the same thread. */
+
+/* activation of gdit_linear */
+#define GDIT_ACT_NONE 0
+#define GDIT_ACT_RELU 1
+#define GDIT_ACT_GELU 2         /* exact: v * Phi(v) */
+#define GDIT_ACT_GELU_TANH 3    /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+#define GDIT_ACT_SILU 4         /* v / (1 + exp(-v)) */
+
+/* norm kinds of gdit_norm_residual */
+#define GDIT_NORM_NONE 0
+#define GDIT_NORM_LAYER 1       /* (t - mean) / sqrt(mean((t - mean)^2) + eps) * gain + bias */
+#define GDIT_NORM_RMS 2         /* t / sqrt(mean(t^2) + eps) * gain + bias */
+
+/* out[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+ *   x         bf16 [m, k], row stride ldx
+ *   w         bf16 [n, k], row stride ldw (PyTorch Linear layout)
+ *   bias      f32 [n] or NULL
+ *   residual  out_dtype [m, n], row stride ldr, or NULL; may be out itself
+ *   out       out_dtype (GDIT_F32 or GDIT_BF16) [m, n], row stride ldo; must
+ *             not overlap x or w
+ * m >= 0; n >= 1; k >= 8, a multiple of 8; x and w 16-byte aligned, ldx and
+ * ldw multiples of 8 and >= k; ldr and ldo >= n; bias, residual and out
+ * aligned to their element. */
+typedef struct {
+  const void* x;
+  const void* w;
+  const float* bias;
+  const void* residual;
+  void* out;
+  int64_t m, ldx, ldw, ldr, ldo;
+  int n, k;
+  int out_dtype;
+  int activation;           /* GDIT_ACT_* */
+} gdit_linear_args;
+
+int gdit_linear(const gdit_linear_args* a, void* cuda_stream);
+
+/* Row by row (row r, width dim, group c = row_group[r]):
+ *   h' = residual_scale h + gate * post(y)      written to out_h
+ *   u  = pre(h') (1 + scale) + shift            written to out_u
+ * u is computed from h' before it is rounded to out_h's type.
+ *   h         h_dtype [rows, dim]: the residual stream
+ *   y         y_dtype [rows, dim]: the block's output, or NULL (h' = residual_scale h)
+ *   out_h     h_dtype [rows, dim], or NULL (not written); may be h itself
+ *   out_u     u_dtype [rows, dim], or NULL (not written); may be y itself if
+ *             the types are equal.  out_h and out_u may not both be NULL.
+ *   post_gain, post_bias, pre_gain, pre_bias   f32 [dim], NULL = 1 or 0
+ *   gate      f32 [gate_groups, dim], NULL = 1
+ *   scale, shift  f32 [mod_groups, dim], NULL = 0
+ *   row_group int32 [rows]: the group of each row, needed when gate_groups or
+ *             mod_groups is above 1; a tensor of one group serves every row
+ * dim in [1, 16384]; strides >= dim; pointers aligned to their element
+ * (16-byte aligned rows of a multiple of 8 elements run fastest). */
+typedef struct {
+  const void* h;
+  const void* y;
+  void* out_h;
+  void* out_u;
+  const float* post_gain;
+  const float* post_bias;
+  const float* gate;
+  const float* pre_gain;
+  const float* pre_bias;
+  const float* scale;
+  const float* shift;
+  const int32_t* row_group;
+  int64_t rows, ldh, ldy, ldoh, ldou;
+  int dim;
+  int h_dtype, y_dtype, u_dtype;
+  int post, pre;            /* GDIT_NORM_* */
+  int gate_groups, mod_groups;
+  float residual_scale, eps;
+} gdit_norm_args;
+
+int gdit_norm_residual(const gdit_norm_args* a, void* cuda_stream);
+
+/* Attention of `batch` packed sequences with grouped heads: sequence b has the
+ * queries cu_q[b] .. cu_q[b+1] and the keys cu_k[b] .. cu_k[b] + nk, with
+ * nk = k_len[b], or cu_k[b+1] - cu_k[b] where k_len is NULL; query head h
+ * reads key head h / (heads / kv_heads).
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = log sum_j exp(scale q_i . k_j)
+ * over the sequence's keys, with causal != 0 only j <= i + (nk - nq): the last
+ * query sees every key, as for a prompt (nq = nk), a further piece of one, and
+ * the next token over a cache (nq = 1).  A query that sees no key has
+ * out = 0 and lse = -infinity.
+ *   q, out    bf16 [total_q, heads, head_dim], k, v bf16 [total_k, kv_heads, head_dim];
+ *             strides of tokens and heads in elements (slices of a fused
+ *             projection are fine); out may be q itself
+ *   lse       f32 [total_q, heads], dense, or NULL
+ *   cu_q, cu_k  int32 [batch + 1]; k_len int32 [batch] or NULL (a slot of a
+ *             cache is then cu_k[b] .. cu_k[b+1], of which k_len[b] are filled)
+ *   max_q, max_k  upper bounds of the sequences' lengths (a longer one is
+ *             reported and skipped)
+ * Rows of out and lse behind the last sequence are left as they were.  Keys
+ * and values outside a sequence (other sequences, unfilled slots) do not
+ * matter, whatever they hold; inside a sequence a value that is not finite
+ * reaches also the queries of which it is hidden.
+ * heads a multiple of kv_heads; heads / kv_heads <= 128; head_dim a multiple
+ * of 8 in [8, 128]; q, k, v 16-byte aligned with strides that are multiples of
+ * 8; total_q, total_k < 2^31; batch in [0, 65535]; scale finite. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* k_len;
+  int64_t total_q, total_k;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+  int batch, heads, kv_heads, head_dim;
+  int max_q, max_k;
+  int causal;
+  float scale;
+} gdit_attention_args;
+
+int gdit_attention(const gdit_attention_args* a, void* cuda_stream);
+
+/* Synchronizes cuda_stream and returns what the operators' kernels on `device`
+ * have reported since the last call: GDIT_OK, GDIT_EDEVICE (bad row_group,
+ * bad sequence offsets) or GDIT_ETIMEOUT (a bounded device wait expired).
+ * Clears it.  One status word per device, shared by all streams. */
+int gdit_op_status(int device, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
