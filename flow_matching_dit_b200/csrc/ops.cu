@@ -31,8 +31,6 @@ int guarded_op(F&& fn) {
   }
 }
 
-constexpr int kMaxDevices = 64;
-
 // The current device, checked once: its SMs.
 int current_sms() {
   static std::mutex mu;
@@ -158,6 +156,7 @@ int gdit_attention(const gdit_attention_args* p, void* cuda_stream) {
             p->head_dim);
     REQUIRE(p->total_q >= 0 && p->total_q <= kMaxRows && p->total_k >= 0 && p->total_k <= kMaxRows,
             "total_q %lld or total_k %lld out of range", (long long)p->total_q, (long long)p->total_k);
+    REQUIRE(p->total_q * (p->heads / p->kv_heads) <= kMaxRows - 256, "total_q * heads / kv_heads out of range");
     REQUIRE(p->max_q >= 0 && p->max_k >= 0, "max_q %d, max_k %d", p->max_q, p->max_k);
     REQUIRE(std::isfinite(p->scale), "scale must be finite");
     if (p->batch == 0 || p->total_q == 0) return;
@@ -166,14 +165,13 @@ int gdit_attention(const gdit_attention_args* p, void* cuda_stream) {
     for (const void* t : {p->q, p->k, p->v}) REQUIRE(aligned_to(t, 16), "q, k and v must be 16-byte aligned");
     for (int64_t s : {p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride, p->v_token_stride,
                       p->v_head_stride})
-      REQUIRE(s >= 0 && s % 8 == 0 && s <= kMaxStride / 2, "stride %lld: not negative, a multiple of 8", (long long)s);
+      REQUIRE(s > 0 && s % 8 == 0 && s <= kMaxStride / 4, "stride %lld: positive and a multiple of 8", (long long)s);
     for (int64_t s : {p->out_token_stride, p->out_head_stride})
-      REQUIRE(s >= 0 && s <= kMaxStride / 2, "out stride %lld", (long long)s);
+      REQUIRE(s > 0 && s <= kMaxStride / 4, "out stride %lld", (long long)s);
     REQUIRE(aligned_to(p->out, 2) && aligned_to(p->lse, 4) && aligned_to(p->cu_q, 4) && aligned_to(p->cu_k, 4) &&
                 aligned_to(p->k_len, 4),
             "out, lse or the offsets not aligned to their elements");
     const int sms = current_sms();
-    (void)sms;
     AttnArgs a;
     a.q = static_cast<const __nv_bfloat16*>(p->q);
     a.k = static_cast<const __nv_bfloat16*>(p->k);
@@ -187,7 +185,9 @@ int gdit_attention(const gdit_attention_args* p, void* cuda_stream) {
     a.batch = p->batch, a.heads = p->heads, a.kv_heads = p->kv_heads, a.dim = p->head_dim;
     a.max_q = p->max_q, a.max_k = p->max_k, a.causal = p->causal != 0;
     a.scale_log2 = p->scale * 1.4426950408889634f;
-    launch_attention(a, (cudaStream_t)cuda_stream);
+    // a score of -infinity (a masked one) times 0 would be NaN; this scale leaves every other score at 0
+    if (std::fabs(a.scale_log2) < 1e-30f) a.scale_log2 = 1e-30f;
+    launch_attention(a, sms, (cudaStream_t)cuda_stream);
   });
 }
 

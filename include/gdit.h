@@ -459,7 +459,7 @@ int gdit_norm_residual(const gdit_norm_args* a, void* cuda_stream);
  * the next token over a cache (nq = 1).  A query that sees no key has
  * out = 0 and lse = -infinity.
  *   q, out    bf16 [total_q, heads, head_dim], k, v bf16 [total_k, kv_heads, head_dim];
- *             strides of tokens and heads in elements (slices of a fused
+ *             positive strides of tokens and heads in elements (slices of a fused
  *             projection are fine); out may be q itself
  *   lse       f32 [total_q, heads], dense, or NULL
  *   cu_q, cu_k  int32 [batch + 1]; k_len int32 [batch] or NULL (a slot of a
@@ -472,7 +472,7 @@ int gdit_norm_residual(const gdit_norm_args* a, void* cuda_stream);
  * reaches also the queries of which it is hidden.
  * heads a multiple of kv_heads; heads / kv_heads <= 128; head_dim a multiple
  * of 8 in [8, 128]; q, k, v 16-byte aligned with strides that are multiples of
- * 8; total_q, total_k < 2^31; batch in [0, 65535]; scale finite. */
+ * 8; total_k and total_q heads / kv_heads below 2^31 - 256; batch in [0, 65535]; scale finite. */
 typedef struct {
   const void* q;
   const void* k;
