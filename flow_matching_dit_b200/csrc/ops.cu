@@ -84,7 +84,6 @@ int gdit_linear(const gdit_linear_args* p, void* cuda_stream) {
     REQUIRE(aligned_to(p->out, es) && aligned_to(p->residual, es) && aligned_to(p->bias, 4),
             "bias, residual or out not aligned to its element");
     const int sms = current_sms();
-    (void)sms;
     LinearArgs a;
     a.x = static_cast<const __nv_bfloat16*>(p->x);
     a.w = static_cast<const __nv_bfloat16*>(p->w);
@@ -95,7 +94,7 @@ int gdit_linear(const gdit_linear_args* p, void* cuda_stream) {
     a.n = p->n, a.k = p->k;
     a.out_f32 = p->out_dtype == GDIT_F32;
     a.act = p->activation;
-    launch_linear(a, (cudaStream_t)cuda_stream);
+    launch_linear(a, sms, (cudaStream_t)cuda_stream);
   });
 }
 

@@ -1,6 +1,16 @@
 // gdit_linear: out[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n].
+//
+// Two kernels, both tcgen05.mma bf16 with f32 accumulators in TMEM, fed by TMA
+// boxes of 64 values of K (128-byte swizzle):
+//   linear_pair_kernel   256 x BN tiles on pairs of CTAs, persistent: the
+//                        epilogue of a tile runs under the products of the next
+//   linear_split_kernel  128 x BN tiles, K cut over the CTAs of a cluster, which
+//                        add their partial tiles through distributed shared
+//                        memory: few rows, few tiles, or an output that TMA
+//                        cannot address
 #pragma once
 
+#include "gemm_tc.cuh"
 #include "ops_common.cuh"
 
 namespace gdit {
@@ -17,59 +27,499 @@ struct LinearArgs {
   int act;
 };
 
-__device__ __forceinline__ float act_value(int act, float v) {
-  switch (act) {
-    case GDIT_ACT_RELU: return v < 0.f ? 0.f : v;   // NaN stays NaN
-    case GDIT_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case GDIT_ACT_GELU_TANH: return 0.5f * v * (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-    case GDIT_ACT_SILU: return v / (1.f + expf(-v));
-    default: return v;
+// Activations in f32.  v / (1 + exp(-v)) with the fast exponential and
+// quotient: a few 2^-22 of the value, 1 + exp overflowing gives 0.
+__device__ __forceinline__ float sigmoid_times(float v, float a) { return __fdividef(v, 1.f + __expf(-a)); }
+
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
+  if (act == GDIT_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];   // NaN stays NaN
+  } else if (act == GDIT_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) gelu_erf2(v[j], v[j + 1]);
+  } else if (act == GDIT_ACT_GELU_TANH) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      v[j] = sigmoid_times(v[j], 1.5957691216057308f * fmaf(0.044715f * v[j] * v[j], v[j], v[j]));
+  } else if (act == GDIT_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = sigmoid_times(v[j], v[j]);
   }
 }
 
-// 64 x 64 outputs a CTA of 256 threads, 4 x 4 a thread, f32 multiply-adds.
-__global__ void __launch_bounds__(256) linear_simple_kernel(const LinearArgs a) {
-  __shared__ float sx[16][68], sw[16][68];
-  pdl_wait();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const long long m0 = (long long)blockIdx.y * 64;
-  const int n0 = blockIdx.x * 64;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.k; k0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int r = i >> 4, c = i & 15;
-      const bool kok = k0 + c < a.k;
-      sx[c][r] = kok && m0 + r < a.m ? __bfloat162float(a.x[(m0 + r) * a.ldx + k0 + c]) : 0.f;
-      sw[c][r] = kok && n0 + r < a.n ? __bfloat162float(a.w[(long long)(n0 + r) * a.ldw + k0 + c]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sx[c][ty * 4 + i], sw[c][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+// ------------------------------------------------------------------ CTA pairs
+//
+// One thread of the even CTA issues the MMAs of both (cta_group::2, 256 x BN x
+// 16): each CTA loads its 128 rows of x and half of the tile's rows of w, and
+// holds its 128 rows of the accumulator.  Eight epilogue warps a CTA, two per
+// 32-lane TMEM quarter, each working through 32-row boxes of 128 bytes of
+// output: TMEM -> bias, activation -> residual (brought into the box by TMA
+// beforehand) -> box -> TMA store.  The boxes of a warp alternate, so that the
+// next residual is on its way while one is used.
+
+constexpr int kLinEpiWarps = 8;
+constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
+
+template <int BN>
+struct LinPairCfg {
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = BN / 2 * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;   // per CTA
+  static constexpr int BOXES = kLinEpiWarps * 2 * 4096;
+  static constexpr int STAGES = (227 * 1024 - 1024 - BOXES - 512) / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + BOXES + 512;
+  static_assert((2 * STAGES + 4 + 2 * kLinEpiWarps) * 8 + 64 <= 512, "barriers");
+};
+
+// Tile t: 256-row block and column tile, row blocks in groups of 8 so that
+// neighbouring tiles share rows of x and of w in L2.
+__device__ __forceinline__ void lin_pair_tile(int t, int mt, int nt, int& mi, int& ni) {
+  const int gs = 8 * nt, g = t / gs, first = g * 8, gm = min(mt - first, 8), r = t - g * gs;
+  mi = first + r % gm;
+  ni = r / gm;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmO,
+                       const LinearArgs a) {
+  using Cfg = LinPairCfg<BN>;
+  constexpr int STAGES = Cfg::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_holder;
+  __shared__ volatile int s_abort;
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * Cfg::A_BYTES;
+  uint8_t* sBox = sB + STAGES * Cfg::B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sBox + Cfg::BOXES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* rfull = tempty + 2;   // 2 a warp
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], 2 * kLinEpiWarps);
+    for (int i = 0; i < 2 * kLinEpiWarps; ++i) mbar_init(&rfull[i], 1);
+    fence_mbar_init();
+    s_abort = 0;
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmO);
   }
-  for (int i = 0; i < 4; ++i) {
-    const long long m = m0 + ty * 4 + i;
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      if (m >= a.m || n >= a.n) continue;
-      float v = act_value(a.act, acc[i][j] + (a.bias ? a.bias[n] : 0.f));
-      if (a.out_f32) {
-        if (a.residual) v += static_cast<const float*>(a.residual)[m * a.ldr + n];
-        static_cast<float*>(a.out)[m * a.ldo + n] = v;
-      } else {
-        if (a.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[m * a.ldr + n]);
-        static_cast<__nv_bfloat16*>(a.out)[m * a.ldo + n] = __float2bfloat16_rn(v);
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_holder, 2 * BN);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  cluster_sync();   // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  const uint32_t full_l = mapa_shared(&full[0], 0), tempty_l = mapa_shared(&tempty[0], 0);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int mt = (int)((a.m + 255) / 256), nt = (a.n + BN - 1) / BN, total = mt * nt;
+  const int nkb = (a.k + 63) / 64;
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  int mi, ni;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = cid; t < total && ok; t += ncl) {
+        lin_pair_tile(t, mt, nt, mi, ni);
+        const int xr = mi * 256 + (int)rank * 128, wr = ni * BN + (int)rank * (BN / 2);
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = op_wait(&empty[stage], phase ^ 1u, &s_abort);
+          if (!ok) break;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * Cfg::STAGE);
+          tma_load_2d_pair(sA + stage * Cfg::A_BYTES, &tmX, full_l + 8u * stage, kb * 64, xr);
+          tma_load_2d_pair(sB + stage * Cfg::B_BYTES, &tmW, full_l + 8u * stage, kb * 64, wr);
+          ++issued;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+      }
+      // every stage has been released by the MMAs' commits, so nothing is pending when the CTA exits
+      const unsigned long long t0 = globaltimer_ns();
+      for (int i = 0; i < min(issued, STAGES); ++i) {
+        while (!mbar_try_wait(&empty[stage], phase ^ 1u) && globaltimer_ns() - t0 < 10000000ull) {
+        }
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = cid; t < total && ok; t += ncl, ++it) {
+        const int buf = it & 1;
+        ok = op_wait(&tempty[buf], ((it >> 1) & 1) ^ 1u, &s_abort);
+        if (!ok) break;
+        tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = op_wait(&full[stage], phase, &s_abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t xa = smem_u32(sA + stage * Cfg::A_BYTES), wa = smem_u32(sB + stage * Cfg::B_BYTES);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16_pair(tmem + buf * BN, smem_desc_sw128(xa + k * 32), smem_desc_sw128(wa + k * 32),
+                           idesc_bf16_f32(256, BN), kb > 0 || k > 0);
+          umma_commit_pair(&empty[stage], 0x3);
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+        umma_commit_pair(&tfull[buf], 0x3);
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+    uint8_t* boxes = sBox + ew * 2 * 4096;
+    const bool bias_vec = ((uintptr_t)a.bias & 15u) == 0;
+    uint64_t* rbar = rfull + 2 * ew;
+    const int cols = a.out_f32 ? 32 : 64, chunks = BN / cols / 2;   // columns of a box, boxes of this warp in a tile
+    const int sw = lane & 7;
+    const bool res = a.residual != nullptr;
+    int it = 0, seq = 0;
+    for (int t = cid; t < total; t += ncl, ++it) {
+      lin_pair_tile(t, mt, nt, mi, ni);
+      const int buf = it & 1, ym = mi * 256 + (int)rank * 128 + q * 32, n0 = ni * BN + half * cols;
+      auto fetch = [&](int s, int n) {   // residual box of chunk s
+        if (lane == 0) {
+          bulk_wait_read<1>();   // the store of chunk s - 2 has left the box
+          mbar_arrive_expect_tx(&rbar[s & 1], 4096);
+          tma_load_2d(boxes + (s & 1) * 4096, &tmR, &rbar[s & 1], n, ym);
+        }
+      };
+      if (res) fetch(seq, n0);
+      if (!op_wait_warp(&tfull[buf], (it >> 1) & 1, &s_abort)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + half * cols;
+      bool ok = true;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++seq) {
+        const int n = n0 + c * 2 * cols;
+        uint8_t* box = boxes + (seq & 1) * 4096;
+        float v[64];
+        tmem_ld32(acc + c * 2 * cols, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+        if (!a.out_f32) tmem_ld32(acc + c * 2 * cols + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+        tmem_ld_wait();
+        if (c == chunks - 1) {   // the accumulator is in registers: the next products may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty_l + 8u * buf);
+        }
+        if (res) {
+          ok = op_wait_warp(&rbar[seq & 1], (seq >> 1) & 1, &s_abort);
+          if (!ok) break;
+        } else {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
+        auto bias_act = [&](float (&x)[32], int nb) {   // the same addresses on all lanes
+          if (a.bias != nullptr) {
+            if (bias_vec && nb + 32 <= a.n) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a.bias + nb + j));
+                x[j] += f.x, x[j + 1] += f.y, x[j + 2] += f.z, x[j + 3] += f.w;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (nb + j < a.n) x[j] += __ldg(a.bias + nb + j);
+            }
+          }
+          apply_act(a.act, x);
+        };
+        uint8_t* brow = box + lane * 128;
+        if (a.out_f32) {
+          bias_act(reinterpret_cast<float(&)[32]>(v[0]), n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float4* p = reinterpret_cast<float4*>(brow + ((j ^ sw) << 4));
+            float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (res) {
+              const float4 r = *p;
+              o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
+            }
+            *p = o;
+          }
+        } else {
+          bias_act(reinterpret_cast<float(&)[32]>(v[0]), n);
+          bias_act(reinterpret_cast<float(&)[32]>(v[32]), n + 32);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4* p = reinterpret_cast<uint4*>(brow + ((j ^ sw) << 4));
+            if (res) {
+              const uint4 r = *p;
+              const float4 r0 = bf16x4_to_f32(make_uint2(r.x, r.y)), r1 = bf16x4_to_f32(make_uint2(r.z, r.w));
+              v[8 * j] += r0.x, v[8 * j + 1] += r0.y, v[8 * j + 2] += r0.z, v[8 * j + 3] += r0.w;
+              v[8 * j + 4] += r1.x, v[8 * j + 5] += r1.y, v[8 * j + 6] += r1.z, v[8 * j + 7] += r1.w;
+            }
+            *p = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                            pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (n < a.n && ym < a.m) tma_store_2d(&tmO, box, n, ym);   // clipped at the matrix' edges
+          bulk_commit();
+        }
+        if (res && c + 1 < chunks) fetch(seq + 1, n + 2 * cols);
+      }
+      if (!ok) break;
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * BN);
+  }
+}
+
+// ------------------------------------------------------------------ split K over a cluster
+//
+// The CTAs of a cluster share one 128 x BN tile and take a part of K each.
+// Every CTA puts its partial tile into its own shared memory (f32, over the
+// spent stages); CTA r then adds the rows r, r + S, ... of all S partial tiles
+// in the order of the parts, so the result does not depend on timing, and
+// writes them with neighbouring columns on neighbouring lanes: any alignment,
+// any width.
+// Rows of x that a tile does not have are not loaded: boxes of `xrows` rows; the
+// MMA reads whatever the shared memory behind them holds into accumulator rows
+// that nobody reads.
+
+constexpr int kSplitThreads = 256;
+
+struct SplitPlan {
+  int bn, splits, stages, xrows;
+  int smem() const { return 1024 + std::max(stages * (xrows + bn) * 128 + (128 - xrows) * 128, 128 * bn * 4) + 512; }
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kSplitThreads)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                        const LinearArgs a, int splits, int stages, int xrows, int smem_bytes) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_holder;
+  __shared__ volatile int s_abort;
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  const int xbytes = xrows * 128, wbytes = BN * 128;
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + stages * xbytes;
+  float* part = reinterpret_cast<float*>(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + smem_bytes - 1024 - 512);
+  uint64_t* empty = full + stages;
+  uint64_t* done = empty + stages;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % splits;
+  const long long tile = blockIdx.x / splits;
+  const int nt = (a.n + BN - 1) / BN;
+  const long long m0 = tile / nt * 128;
+  const int n0 = (int)(tile % nt) * BN;
+  const int nkb = (a.k + 63) / 64;
+  const int kb0 = (int)((long long)rank * nkb / splits), kb1 = (int)((long long)(rank + 1) * nkb / splits);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    mbar_init(done, 1);
+    fence_mbar_init();
+    s_abort = 0;
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_holder, BN);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 0 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!op_wait(&empty[stage], phase ^ 1u, &s_abort)) {
+        // only after a wait has run out: the loads under way land before the CTA leaves
+        for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) {
+        }
+        break;
+      }
+      mbar_arrive_expect_tx(&full[stage], xbytes + wbytes);
+      tma_load_2d(sB + stage * wbytes, &tmW, &full[stage], kb * 64, n0);
+      tma_load_2d(sA + stage * xbytes, &tmX, &full[stage], kb * 64, (int)m0);
+      if (++stage == stages) stage = 0, phase ^= 1u;
+    }
+  } else if (warp == 1 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!op_wait(&full[stage], phase, &s_abort)) break;
+      tc_fence_after();
+      const uint32_t xa = smem_u32(sA + stage * xbytes), wa = smem_u32(sB + stage * wbytes);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        umma_bf16(tmem, smem_desc_sw128(xa + k * 32), smem_desc_sw128(wa + k * 32), idesc_bf16_f32(128, BN),
+                  kb > kb0 || k > 0);
+      umma_commit(&empty[stage]);
+      if (++stage == stages) stage = 0, phase ^= 1u;
+    }
+    umma_commit(done);
+  }
+  __syncwarp();
+  // the products are complete, so every load has landed and every stage has been read
+  const bool ok = op_wait_warp(done, 0, &s_abort);
+  __syncthreads();
+  tc_fence_after();
+  const int rows = (int)min((long long)128, a.m - m0);
+  const int q = warp & 3;
+  if (ok && q * 32 < rows) {
+    const int row = q * 32 + lane;
+#pragma unroll 1
+    for (int c = (warp >> 2) * 32; c < BN; c += 64) {
+      uint32_t r[32];
+      tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, r);
+      tmem_ld_wait();
+      if (row < rows) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)   // 16-byte pieces of a row in an order of its own: no bank conflicts
+          *reinterpret_cast<uint4*>(part + row * BN + ((((c >> 2) + j) ^ (row & 7)) << 2)) =
+              make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
       }
     }
   }
+  tc_fence_before();
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
+  if (ok) {
+    uint32_t base[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) base[s] = s < splits ? (splits > 1 ? mapa_shared(part, s) : smem_u32(part)) : 0;
+    // a warp takes a row's 32 columns at a time
+    const int groups = BN / 32;
+    for (int u = warp; u < (rows - rank + splits - 1) / splits * groups; u += kSplitThreads / 32) {
+      const int row = rank + u / groups * splits, col = (u % groups) * 32 + lane, n = n0 + col;
+      const uint32_t at = (uint32_t)(row * BN + (((col >> 2) ^ (row & 7)) << 2) + (col & 3)) * 4u;
+      float part_s[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < splits) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part_s[s]) : "r"(base[s] + at));
+      float v[2] = {part_s[0], 0.f};
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < splits) v[0] += part_s[s];
+      if (n < a.n) {
+        const long long m = m0 + row;
+        if (a.bias != nullptr) v[0] += a.bias[n];
+        apply_act(a.act, v);
+        if (a.out_f32) {
+          if (a.residual != nullptr) v[0] += static_cast<const float*>(a.residual)[m * a.ldr + n];
+          static_cast<float*>(a.out)[m * a.ldo + n] = v[0];
+        } else {
+          if (a.residual != nullptr)
+            v[0] += __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[m * a.ldr + n]);
+          static_cast<__nv_bfloat16*>(a.out)[m * a.ldo + n] = __float2bfloat16_rn(v[0]);
+        }
+      }
+    }
+  }
+  if (splits > 1) cluster_sync();   // nobody leaves while its partial tile is read
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, BN);
+  }
 }
 
-inline void launch_linear(const LinearArgs& a, cudaStream_t s) {
-  launch_op(s, 1, linear_simple_kernel, dim3((a.n + 63) / 64, (unsigned)((a.m + 63) / 64)), dim3(256), 0, a);
+// ------------------------------------------------------------------ planning and launches
+
+// [rows, cols] of the output type, boxes of 32 rows x 128 bytes, 128-byte swizzle.
+inline CUtensorMap make_box_tmap(const void* p, int f32, long long rows, long long cols, long long ld) {
+  CUtensorMap m;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld * (f32 ? 4 : 2))};
+  cuuint32_t box[2] = {f32 ? 32u : 64u, 32u};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = encode_fn()(&m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                           const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) throw GditError(GDIT_ECUDA, fmt("cuTensorMapEncodeTiled (output) failed (%d)", (int)r));
+  return m;
+}
+
+template <int BN>
+void launch_linear_pair(const LinearArgs& a, int sms, cudaStream_t s) {
+  using Cfg = LinPairCfg<BN>;
+  const CUtensorMap tx = make_tmap(a.x, a.m, a.k, a.ldx, 128), tw = make_tmap(a.w, a.n, a.k, a.ldw, BN / 2);
+  const CUtensorMap to = make_box_tmap(a.out, a.out_f32, a.m, a.n, a.ldo);
+  const CUtensorMap tr = a.residual != nullptr ? make_box_tmap(a.residual, a.out_f32, a.m, a.n, a.ldr) : to;
+  const long long tiles = (a.m + 255) / 256 * ((a.n + BN - 1) / BN);
+  REQUIRE(tiles <= INT32_MAX / 2, "m %lld x n %d has too many tiles", a.m, a.n);
+  allow_smem(linear_pair_kernel<BN>, Cfg::SMEM);
+  launch_op(s, 2, linear_pair_kernel<BN>, dim3((unsigned)(2 * std::min<long long>(tiles, sms / 2))), dim3(kLinThreads),
+            Cfg::SMEM, tx, tw, tr, to, a);
+}
+
+template <int BN>
+void launch_linear_split(const LinearArgs& a, const SplitPlan& p, cudaStream_t s) {
+  const CUtensorMap tx = make_tmap(a.x, a.m, a.k, a.ldx, p.xrows), tw = make_tmap(a.w, a.n, a.k, a.ldw, BN);
+  const long long tiles = (a.m + 127) / 128 * ((a.n + BN - 1) / BN);
+  REQUIRE(tiles * p.splits <= INT32_MAX, "m %lld x n %d has too many tiles", a.m, a.n);
+  allow_smem(linear_split_kernel<BN>, 226 * 1024);   // the kernel has some bytes of its own
+  launch_op(s, p.splits, linear_split_kernel<BN>, dim3((unsigned)(tiles * p.splits)), dim3(kSplitThreads), p.smem(), tx,
+            tw, a, p.splits, p.stages, p.xrows, p.smem());
+}
+
+inline SplitPlan plan_split(long long m, int n, int k, int sms) {
+  SplitPlan p;
+  const int nkb = (k + 63) / 64;
+  const long long mt = (m + 127) / 128;
+  auto tiles = [&](int bn) { return mt * ((n + bn - 1) / bn); };
+  // the widest tiles that still give every SM one, with K cut over up to 8 CTAs
+  p.bn = tiles(128) * std::min(8, std::max(1, nkb / 4)) >= sms ? 128 : tiles(64) * std::min(8, std::max(1, nkb / 4)) >= sms ? 64 : 32;
+  p.splits = 1;
+  while (p.splits < 8 && 2 * p.splits * 2 <= nkb && tiles(p.bn) * p.splits < sms) p.splits *= 2;
+  p.xrows = m >= 96 ? 128 : m > 32 ? 64 : 32;
+  if (m > 64) p.xrows = 128;
+  const int per = (nkb + p.splits - 1) / p.splits;
+  const int budget = (tiles(p.bn) * p.splits > sms ? 110 : 220) * 1024 - 2048 - (128 - p.xrows) * 128;
+  p.stages = std::max(2, std::min({per, 16, budget / ((p.xrows + p.bn) * 128)}));
+  return p;
+}
+
+inline void launch_linear(const LinearArgs& a, int sms, cudaStream_t s) {
+  const int es = a.out_f32 ? 4 : 2;
+  auto tma_ok = [&](const void* p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld * es % 16 == 0; };
+  const bool tma = tma_ok(a.out, a.ldo) && (a.residual == nullptr || tma_ok(a.residual, a.ldr));
+  const long long mt = (a.m + 255) / 256;
+  if (tma && mt * ((a.n + 127) / 128) >= sms / 2) {
+    if (mt * ((a.n + 255) / 256) >= sms / 2) launch_linear_pair<256>(a, sms, s);
+    else launch_linear_pair<128>(a, sms, s);
+    return;
+  }
+  const SplitPlan p = plan_split(a.m, a.n, a.k, sms);
+  if (p.bn == 128) launch_linear_split<128>(a, p, s);
+  else if (p.bn == 64) launch_linear_split<64>(a, p, s);
+  else launch_linear_split<32>(a, p, s);
 }
 
 }  // namespace gdit
