@@ -1,6 +1,7 @@
 // gdit_attention: softmax attention over packed sequences with grouped heads.
 #pragma once
 
+#include "gemm_tc.cuh"
 #include "ops_common.cuh"
 
 namespace gdit {
@@ -54,120 +55,172 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
   if (bad) atomicOr(&g_op_status, OP_ERR_OFFSETS);
 }
 
-// ------------------------------------------------------------------ tensor-core kernel
+// ------------------------------------------------------------------ the kernel
 //
-// The queries of one key head are taken as packed rows r = position * group +
-// head in the group, so that the heads that share keys share a tile: the keys
-// are read once for all of them, and a causal tile of 256 rows spans only
-// 256 / group positions.  A CTA works on tiles of 256 rows as two halves of
-// 128, each with a softmax warpgroup of its own: while one half's scores are
-// turned into probabilities, the tensor core multiplies for the other.
+// The queries of one key head are taken as packed rows i = position * group +
+// head in the group, so that the heads that share keys share a tile and the
+// keys are read once for all of them.  128 rows (128 / group whole positions,
+// one 3-D TMA box) make a half; a CTA has two halves, each with a softmax
+// warpgroup, scores and an output of its own in TMEM, so that one half's scores
+// are turned into probabilities while the tensor core multiplies for the other.
 //
-//   warp 0       K and V tiles of 128 keys by TMA into a ring of SLOTS tiles
-//   warp 1       tcgen05.mma: S = Q K^T (f32, TMEM), O += P V (P from TMEM)
-//   warps 2, 3   Q rows by cp.async; warp 3 also zeroes the rows of the last V tile that no row of the tile sees
+//   rows kernel (KEYS = false)  the halves are neighbouring positions and go over the same keys: prompts
+//   keys kernel (KEYS = true)   the halves have the same rows and take turns at the blocks of 128 keys, and the CTAs of a
+//                               cluster take a part of the keys each: single tokens and too few tiles for the SMs.  The
+//                               partial outputs are joined in the order of the parts, through distributed shared memory.
+//
+//   warp 0       Q boxes, K and V tiles of 128 keys by TMA; K and V in a ring of SLOTS tiles in the order of their use
+//   warp 1       tcgen05.mma: S = Q K^T (f32, TMEM), O += P V (P from TMEM); zeroes the rows of the last V tile that lie
+//                behind the tile's last key within 16, since 0 times what they hold may be NaN
+//   warp 2       reports bad sequences
 //   warps 4-11   softmax of one half each: thread = row; P (bf16) overwrites S; O is rescaled only when the running maximum
 //                has grown by more than 2^8 (the statistics refer to the maximum in use, so nothing is lost), and
 //                divided by the sum at the end
 //
-// The tensor core executes in issue order P V (j), Q K^T (j + 1) of one half,
-// then of the other, so a full S (j + 1) also says that O holds the blocks up
-// to j.  Tiles are walked in a static order, the longest of a sequence first.
+// The tensor core executes in issue order P V (j), Q K^T (next block) of one
+// half, then of the other, so a full S also says that O holds the blocks before.
 
 constexpr int kAtBM = 128;       // rows of a half
 constexpr int kAtBN = 128;       // keys of a block
 constexpr int kAtThreads = 384;
+// Registers of a thread: 168 at launch (64512 in all), then 72 for the first
+// warpgroup and 216 for the softmax ones (the same 64512).
+constexpr int kAtRegs = 168, kAtRegsIssue = 72, kAtRegsSoftmax = 216;
+static_assert(3 * kAtRegs == kAtRegsIssue + 2 * kAtRegsSoftmax, "register split");
 
-template <int DP>   // head_dim rounded up to 64 or 128
+template <int DP, bool KEYS>   // head_dim rounded up to 64 or 128
 struct AttnCfg {
   static constexpr int BOX = kAtBN * 128;                    // bytes of a [128][64] box
   static constexpr int TILE = BOX * (DP / 64);
-  static constexpr int SLOTS = DP == 128 ? 5 : 10;
-  static constexpr int SMEM = 1024 + 2 * TILE + SLOTS * TILE + 256;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr int Q = (KEYS ? 1 : 2) * TILE;
+  static constexpr int PART = KEYS ? kAtBM * DP * 4 : 0;     // f32 partial output of the CTA
+  static constexpr int STATS = KEYS ? kAtBM * 8 : 0;         // maximum and sum of its rows
+  static constexpr int BARS = 384;
+  static constexpr int RING = 227 * 1024 - 128 - 1024 - Q - PART - STATS - BARS;   // 128: static shared memory
+  static constexpr int SLOTS = RING / TILE < 10 ? RING / TILE : 10;
+  static constexpr int SMEM = 1024 + Q + PART + STATS + BARS + SLOTS * TILE;
+  static_assert((2 * SLOTS + 16) * 8 <= BARS, "barriers");
 };
 
-// A tile: rows [r0, r0 + rows) of sequence s and key head kvh, the first
-// `blocks` key blocks, of which the keys below `end` are seen by some row.
+// A tile: positions [p0, p0 + np) of sequence s and the heads of key head kvh.
+// Some row sees the keys below `end`; this CTA takes the key blocks [b0, b0 + nb).
 struct AttnTile {
   Seq s;
-  int r0, rows, kvh, end, blocks;
+  int p0, np, kvh, end, b0, nb;
 };
 
-// Walks the tiles t, t + step, ... of the call: all lanes of a warp together.
-// A group of 32 sequences at a time, lane i looks after sequence base + i.
+// Walks tiles in an order that all warps and CTAs agree on: all lanes of a warp
+// together.  A group of 32 sequences at a time, one a lane; within a group by
+// falling position (the longest tiles of causal prompts first), and in the keys
+// kernel by falling number of keys.
 struct TileWalk {
   int base;              // first sequence of the group
-  long long before;      // tiles in front of it
-  int incl;              // lane: tiles of the group up to and with this sequence
-  int mine;
+  long long before;      // tiles in front of the group
+  int level, full;       // tiles `level` and up of the group's sequences: `full` in number, those above `level`: `above`
+  int above;
+  int mine;              // lane: tiles of its sequence
   Seq seq;
 
-  __device__ __forceinline__ void load(const AttnArgs& a, int tile_rows) {
-    const int lane = threadIdx.x & 31, b = base + lane;
+  template <bool KEYS>
+  __device__ __forceinline__ void load(const AttnArgs& a, int tile_pos) {
+    const int lane = threadIdx.x & 31;
     seq = {0, 0, 0, 0};
-    mine = 0;
-    if (b < a.batch) {
+    if (base + lane < a.batch) {
       bool ok;
-      const Seq s = read_seq(a, b, ok);
-      if (ok) {
-        seq = s;
-        mine = (int)(((long long)s.nq * (a.heads / a.kv_heads) + tile_rows - 1) / tile_rows);
-      }
+      const Seq s = read_seq(a, base + lane, ok);
+      if (ok) seq = s;
     }
-    incl = mine;
+    if (KEYS) {   // most keys first, so that the last tiles to be handed out are short
+      int rank = 0, src = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += x;
+      for (int i = 0; i < 32; ++i) {
+        const int nk = __shfl_sync(~0u, seq.nk, i);
+        rank += nk > seq.nk || (nk == seq.nk && i < lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) src = __shfl_sync(~0u, rank, i) == lane ? i : src;
+      seq.q0 = __shfl_sync(~0u, seq.q0, src);
+      seq.nq = __shfl_sync(~0u, seq.nq, src);
+      seq.k0 = __shfl_sync(~0u, seq.k0, src);
+      seq.nk = __shfl_sync(~0u, seq.nk, src);
     }
+    mine = seq.nq / tile_pos + (seq.nq % tile_pos != 0);
+    level = __reduce_max_sync(~0u, mine);
+    full = above = 0;
   }
 
-  __device__ __forceinline__ void start(const AttnArgs& a, int tile_rows) {
+  template <bool KEYS>
+  __device__ __forceinline__ void start(const AttnArgs& a, int tile_pos) {
     base = 0;
     before = 0;
-    load(a, tile_rows);
+    load<KEYS>(a, tile_pos);
   }
 
-  // id = tile * kv_heads + key head; false behind the last tile
-  __device__ __forceinline__ bool at(const AttnArgs& a, int tile_rows, long long id, AttnTile& t) {
-    const int kvh = (int)(id % a.kv_heads);
+  // id = tile * kv_heads + key head, growing from call to call; false behind the last tile
+  template <bool KEYS>
+  __device__ __forceinline__ bool at(const AttnArgs& a, int tile_pos, long long id, int rank, int splits, AttnTile& t) {
     const long long n = id / a.kv_heads;
+    t.kvh = (int)(id - n * a.kv_heads);
     if (n >= a.max_tiles) return false;
-    while (true) {
-      const int total = __shfl_sync(~0u, incl, 31);
-      if (n < before + total) break;
-      before += total;
-      base += 32;
-      if (base >= a.batch) return false;
-      load(a, tile_rows);
+    const int lane = threadIdx.x & 31;
+    while (n - before >= full) {   // the next level, or the next group
+      if (level == 0) {
+        before += full;
+        base += 32;
+        if (base >= a.batch) return false;
+        load<KEYS>(a, tile_pos);
+        continue;
+      }
+      --level;
+      above = full;
+      full += __popc(__ballot_sync(~0u, mine > level));
     }
-    const int rel = (int)(n - before);
-    const int src = __popc(__ballot_sync(~0u, incl <= rel));
+    const unsigned there = __ballot_sync(~0u, mine > level);
+    const int nth = (int)(n - before) - above;
+    const int src = __ffs(__ballot_sync(~0u, mine > level && __popc(there & ((1u << lane) - 1)) == nth)) - 1;
     t.s.q0 = __shfl_sync(~0u, seq.q0, src);
     t.s.nq = __shfl_sync(~0u, seq.nq, src);
     t.s.k0 = __shfl_sync(~0u, seq.k0, src);
     t.s.nk = __shfl_sync(~0u, seq.nk, src);
-    const int last = __shfl_sync(~0u, incl, src) - 1 - rel;   // the last tile of a sequence first
-    const int group = a.heads / a.kv_heads;
-    t.kvh = kvh;
-    t.r0 = last * tile_rows;
-    t.rows = min(tile_rows, t.s.nq * group - t.r0);
+    t.p0 = level * tile_pos;
+    t.np = min(tile_pos, t.s.nq - t.p0);
     t.end = t.s.nk;
-    if (a.causal) t.end = max(0, min(t.s.nk, (t.r0 + t.rows - 1) / group + t.s.nk - t.s.nq + 1));
-    t.blocks = (t.end + kAtBN - 1) / kAtBN;
+    if (a.causal) t.end = max(0, min(t.s.nk, t.p0 + t.np + t.s.nk - t.s.nq));
+    const int blocks = (t.end + kAtBN - 1) / kAtBN;
+    t.b0 = KEYS ? (int)((long long)rank * blocks / splits) : 0;
+    t.nb = KEYS ? (int)((long long)(rank + 1) * blocks / splits) - t.b0 : blocks;
     return true;
   }
 };
 
-__device__ __forceinline__ void store_out_row(__nv_bfloat16* o, int vec, int c0, int dim, const float (&v)[32]) {
-  if (vec) {
+// Position r of a walk over `count` workers in rounds that run back and forth:
+// with tiles of falling length everybody gets as much.
+__device__ __forceinline__ long long snake(long long round, int worker, int count) {
+  return round * count + ((round & 1) ? count - 1 - worker : worker);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// mode 2: rows aligned to 32 bytes, 1: to 16 bytes, 0: to their elements
+__device__ __forceinline__ void store_out_row(__nv_bfloat16* o, int mode, int c0, int dim, const float (&v)[32]) {
+  uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 32; j += 8)
-      if (c0 + j < dim)
-        *reinterpret_cast<uint4*>(o + c0 + j) =
-            make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]), pack_bf16x2(v[j + 4], v[j + 5]),
-                       pack_bf16x2(v[j + 6], v[j + 7]));
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  if (mode == 2 && c0 + 32 <= dim) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + c0 + 2 * j), "r"(w[j]),
+                   "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]), "r"(w[j + 6]), "r"(w[j + 7])
+                   : "memory");
+  } else if (mode >= 1) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4)
+      if (c0 + 2 * j < dim)
+        *reinterpret_cast<uint4*>(o + c0 + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -175,38 +228,46 @@ __device__ __forceinline__ void store_out_row(__nv_bfloat16* o, int vec, int c0,
   }
 }
 
-template <int DP>
+template <int DP, bool KEYS>
 __global__ void __launch_bounds__(kAtThreads, 1)
-    attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const AttnArgs a, int tile_rows, int out_vec) {
-  using Cfg = AttnCfg<DP>;
+    attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a, int splits, int out_mode) {
+  using Cfg = AttnCfg<DP, KEYS>;
   constexpr int SLOTS = Cfg::SLOTS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int s_abort;
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-  uint8_t* sQ = smem;                        // two halves
-  uint8_t* sKV = smem + 2 * Cfg::TILE;       // ring
-  uint64_t* full = reinterpret_cast<uint64_t*>(sKV + SLOTS * Cfg::TILE);
+  uint8_t* sQ = smem;
+  uint8_t* sKV = sQ + Cfg::Q;
+  float* part = reinterpret_cast<float*>(sKV + SLOTS * Cfg::TILE);
+  float2* stats = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(part) + Cfg::PART);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stats) + Cfg::STATS);
   uint64_t* empty = full + SLOTS;
   uint64_t* qfull = empty + SLOTS;
   uint64_t* qempty = qfull + 1;
-  uint64_t* vfix = qempty + 1;
-  uint64_t* vgo = vfix + 1;
-  uint64_t* sfull = vgo + 1;                 // [2]
-  uint64_t* pfull = sfull + 2;               // [2]
-  uint64_t* ofull = pfull + 2;               // [2]
+  uint64_t* sfull = qempty + 1;              // [2]
+  uint64_t* pfull = sfull + 2;               // [2][2]: the first and the other 64 keys of a block
+  uint64_t* ofull = pfull + 4;               // [2]
+  uint64_t* hfull = ofull + 2;               // half 1's part is in shared memory
+  uint64_t* jfull = hfull + 1;               // the parts of all CTAs are
+  uint64_t* jempty = jfull + 1;              // and have been read by all
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = KEYS ? (int)(blockIdx.x % splits) : 0;
+  const int worker = blockIdx.x / splits, workers = gridDim.x / splits;
   if (threadIdx.x == 0) {
     for (int i = 0; i < SLOTS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    mbar_init(qfull, 64);
+    mbar_init(qfull, 1);
     mbar_init(qempty, 1);
-    mbar_init(vfix, 1);
-    mbar_init(vgo, 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&sfull[s], 1), mbar_init(&pfull[s], 4), mbar_init(&ofull[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&sfull[s], 1), mbar_init(&ofull[s], 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&pfull[s], 4);
+    mbar_init(hfull, 4);
+    mbar_init(jfull, 4 * splits);
+    mbar_init(jempty, 8 * splits);
     fence_mbar_init();
     s_abort = 0;
+    tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -215,204 +276,215 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  __syncthreads();
+  if (KEYS && splits > 1) cluster_sync();   // all CTAs' barriers exist before any is signalled from outside
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
   pdl_wait();
   pdl_launch_dependents();
 
   const int group = a.heads / a.kv_heads;
-  const int ksteps = (a.dim + 15) / 16;
+  const int half_pos = kAtBM / group;                 // positions of a half
+  const int tile_pos = KEYS ? half_pos : 2 * half_pos;
   TileWalk walk;
   AttnTile t;
-  walk.start(a, tile_rows);
+  bool ok = true;
 
-  if (warp == 0) {
-    int slot = 0;
-    uint32_t phase = 0;
-    int issued = 0, nfix = 0;
-    bool ok = true;
-    for (long long id = blockIdx.x; walk.at(a, tile_rows, id, t) && ok; id += gridDim.x) {
-      if (lane == 0) {
-        for (int j = 0; j < 2 * t.blocks && ok; ++j) {
-          ok = op_wait(&empty[slot], phase ^ 1u, &s_abort);
-          if (!ok) break;
-          uint8_t* dst = sKV + slot * Cfg::TILE;
-          const CUtensorMap* map = (j & 1) ? &tmV : &tmK;
-          const int boxes = a.dim > 64 ? 2 : 1;
-          mbar_arrive_expect_tx(&full[slot], boxes * Cfg::BOX);
-          for (int x = 0; x < boxes; ++x)
-            tma_load_3d(dst + x * Cfg::BOX, map, &full[slot], x * 64, t.kvh, t.s.k0 + (j >> 1) * kAtBN);
-          ++issued;
-          if (++slot == SLOTS) slot = 0, phase ^= 1u;
+  if (warp < 4) {
+    set_max_regs_dec<kAtRegsIssue>();
+    if (warp == 0) {
+      walk.start<KEYS>(a, tile_pos);
+      int slot = 0, nq = 0;
+      uint32_t phase = 0;
+      const int boxes = a.dim > 64 ? 2 : 1;
+      for (long long round = 0;
+           ok && walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
+        if (t.nb == 0) continue;
+        if (lane == 0) {
+          ok = op_wait(qempty, (nq & 1) ^ 1u, &s_abort);
+          if (ok) {
+            const int halves = !KEYS && t.np > half_pos ? 2 : 1;
+            mbar_arrive_expect_tx(qfull, halves * boxes * half_pos * group * 128);
+            for (int s = 0; s < halves; ++s)
+              for (int x = 0; x < boxes; ++x)
+                tma_load_3d(sQ + s * Cfg::TILE + x * Cfg::BOX, &tmQ, qfull, x * 64, t.kvh * group,
+                            t.s.q0 + t.p0 + s * half_pos);
+          }
+          // the order of use: K of the first block (first two in the keys kernel), then V of a block and K of a later one in turn
+          const int ahead = KEYS ? min(2, t.nb) : 1, turns = 2 * (t.nb - ahead);
+          for (int i = 0; i < 2 * t.nb && ok; ++i) {
+            const int u = i - ahead;
+            const bool is_v = u >= 0 && (u >= turns || (u & 1) == 0);
+            const int j = u < 0 ? i : u >= turns ? t.nb - ahead + u - turns : (u & 1) ? ahead + (u >> 1) : u >> 1;
+            ok = op_wait(&empty[slot], phase ^ 1u, &s_abort);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&full[slot], boxes * Cfg::BOX);
+            for (int x = 0; x < boxes; ++x)
+              tma_load_3d(sKV + slot * Cfg::TILE + x * Cfg::BOX, is_v ? &tmV : &tmK, &full[slot], x * 64, t.kvh,
+                          t.s.k0 + (t.b0 + j) * kAtBN);
+            if (++slot == SLOTS) slot = 0, phase ^= 1u;
+          }
+          if (!ok) {   // only after a wait has run out: the loads under way land before the CTA leaves
+            for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) {
+            }
+          }
         }
-        if (ok && (t.end & 15)) {
-          // the last V tile has been asked for: warp 3 may wait for it (the
-          // one before it is done, so that vgo is never two phases ahead)
-          if (nfix > 0) ok = op_wait(vfix, (nfix - 1) & 1, &s_abort);
-          if (ok) mbar_arrive(vgo);
-          ++nfix;
-        }
+        ++nq;
+        ok = __shfl_sync(~0u, ok, 0);
       }
-      ok = __shfl_sync(~0u, ok, 0);
-    }
-    // nothing of this CTA's is in flight when it exits, whatever happened
-    if (lane == 0) {
-      for (int i = 0; i < min(issued, SLOTS); ++i) {
-        if (slot == 0) phase ^= 1u;
-        slot = slot == 0 ? SLOTS - 1 : slot - 1;
-        const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_try_wait(&full[slot], phase) && globaltimer_ns() - t0 < 10000000ull) {
-        }
-      }
-    }
-  } else if (warp == 1) {
-    const uint32_t idesc_qk = idesc_bf16_f32(kAtBM, kAtBN) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);   // -Q for a negative scale
-    const uint32_t idesc_pv = idesc_bf16_f32(kAtBM, (a.dim + 15) / 16 * 16) | (1u << 16);            // V: N-major
-    int slot = 0, nq = 0, nfix = 0;
-    uint32_t phase = 0, pphase[2] = {0, 0};
-    bool ok = true;
-    for (long long id = blockIdx.x; walk.at(a, tile_rows, id, t) && ok; id += gridDim.x) {
-      if (t.blocks == 0) continue;
-      if (lane == 0) {
-        const int halves = t.rows > kAtBM ? 2 : 1;
-        auto qk = [&](int s, int sl) {
-          const uint32_t q = smem_u32(sQ + s * Cfg::TILE), k = smem_u32(sKV + sl * Cfg::TILE);
+    } else if (warp == 1) {
+      walk.start<KEYS>(a, tile_pos);
+      const uint32_t idesc_qk = idesc_bf16_f32(kAtBM, kAtBN) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);   // -Q for a negative scale
+      const uint32_t idesc_pv = idesc_bf16_f32(kAtBM, (a.dim + 15) / 16 * 16) | (1u << 16);            // V: N-major
+      const int ksteps = (a.dim + 15) / 16;
+      int slot = 0, nq = 0;
+      uint32_t phase = 0, pphase = 0;   // pphase: bit s for half s
+      auto next = [&] {
+        if (++slot == SLOTS) slot = 0, phase ^= 1u;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (lane == 0) umma_commit(bar);
+        __syncwarp();
+      };
+      auto qk = [&](int s, int sl) {
+        if (lane == 0) {
+          const uint32_t q = smem_u32(sQ + (KEYS ? 0 : s * Cfg::TILE)), k = smem_u32(sKV + sl * Cfg::TILE);
           for (int x = 0; x < ksteps; ++x) {
             const uint32_t o = (x >> 2) * Cfg::BOX + (x & 3) * 32;
             umma_bf16(tmem + s * kAtBN, smem_desc_sw128(q + o), smem_desc_sw128(k + o), idesc_qk, x > 0);
           }
           umma_commit(&sfull[s]);
-        };
-        auto next = [&] {
-          if (++slot == SLOTS) slot = 0, phase ^= 1u;
-        };
-        ok = op_wait(qfull, nq & 1, &s_abort) && op_wait(&full[slot], phase, &s_abort);
-        if (ok) {
+        }
+        __syncwarp();
+      };
+      // P V of half s over the steps [x0, x1) of 16 keys
+      auto pv = [&](int s, int sl, int x0, int x1, bool first) {
+        if (lane == 0) {
+          const uint32_t v = smem_u32(sKV + sl * Cfg::TILE);
+          for (int x = x0; x < x1; ++x)
+            umma_bf16_ts(tmem + 2 * kAtBN + s * 128, tmem + s * kAtBN + x * 8,
+                         smem_desc_mn_sw128(v + x * 2048, Cfg::BOX), idesc_pv, !first || x > 0);
+        }
+        __syncwarp();
+      };
+      // V of block j is there, and zero where its last 16 keys lie behind the tile's last one
+      auto wait_v = [&](int sl, uint32_t ph, int keys) {
+        if (!op_wait_all(&full[sl], ph, &s_abort)) return false;
+        if (keys & 15) {
+          uint8_t* v = sKV + sl * Cfg::TILE;
+          for (int i = lane; i < (16 - (keys & 15)) * (DP / 8); i += 32) {
+            const int row = keys + i / (DP / 8), c = i % (DP / 8);
+            *reinterpret_cast<uint4*>(v + (c >> 3) * Cfg::BOX + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        return true;
+      };
+      for (long long round = 0;
+           ok && walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
+        if (t.nb == 0) continue;
+        const int halves = !KEYS && t.np > half_pos ? 2 : 1;   // that share each block
+        ok = op_wait_all(qfull, nq & 1, &s_abort);
+        ++nq;
+        const int ahead = KEYS ? min(2, t.nb) : 1;
+        for (int j = 0; j < ahead && ok; ++j) {
+          ok = op_wait_all(&full[slot], phase, &s_abort);
+          if (!ok) break;
           tc_fence_after();
-          for (int s = 0; s < halves; ++s) qk(s, slot);
-          umma_commit(&empty[slot]);
+          for (int s = 0; s < halves; ++s) qk(KEYS ? j : s, slot);
+          commit(&empty[slot]);
           next();
         }
-        for (int j = 0; j < t.blocks && ok; ++j) {
+        if (t.nb <= ahead) commit(qempty);
+        for (int j = 0; j < t.nb && ok; ++j) {
           const int vslot = slot;
           const uint32_t vphase = phase;
           next();
-          const bool more = j + 1 < t.blocks;
-          const int keys = min(kAtBN, t.end - j * kAtBN);
-          for (int s = 0; s < halves && ok; ++s) {
-            ok = op_wait(&pfull[s], pphase[s], &s_abort);
-            pphase[s] ^= 1u;
-            if (ok && s == 0) {
-              ok = op_wait(&full[vslot], vphase, &s_abort);
-              if (ok && !more && (keys & 15)) ok = op_wait(vfix, nfix++ & 1, &s_abort);
-            }
+          const bool more = j + ahead < t.nb;
+          const int keys = min(kAtBN, t.end - (t.b0 + j) * kAtBN), steps = (keys + 15) / 16;
+          for (int h = 0; h < halves && ok; ++h) {
+            const int s = KEYS ? j & 1 : h;
+            const bool first = j < (KEYS ? 2 : 1);
+            if (h == 0) ok = wait_v(vslot, vphase, keys);
+            ok = ok && op_wait_all(&pfull[2 * s], (pphase >> s) & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v = smem_u32(sKV + vslot * Cfg::TILE);
-            for (int x = 0; x < (keys + 15) / 16; ++x)
-              umma_bf16_ts(tmem + 2 * kAtBN + s * 128, tmem + s * kAtBN + x * 8,
-                           smem_desc_mn_sw128(v + x * 2048, Cfg::BOX), idesc_pv, j > 0 || x > 0);
-            if (s == halves - 1) umma_commit(&empty[vslot]);
+            pv(s, vslot, 0, min(4, steps), first);
+            ok = op_wait_all(&pfull[2 * s + 1], (pphase >> s) & 1u, &s_abort);
+            pphase ^= 1u << s;
+            if (!ok) break;
+            tc_fence_after();
+            pv(s, vslot, 4, steps, first);
+            if (h == halves - 1) commit(&empty[vslot]);
             if (more) {
-              if (s == 0) ok = op_wait(&full[slot], phase, &s_abort);
+              if (h == 0) ok = op_wait_all(&full[slot], phase, &s_abort);
               if (!ok) break;
               tc_fence_after();
               qk(s, slot);
-              if (s == halves - 1) umma_commit(&empty[slot]);
+              if (h == halves - 1) {
+                commit(&empty[slot]);
+                if (j + ahead == t.nb - 1) commit(qempty);   // Q has been used for the last time
+              }
             } else {
-              umma_commit(&ofull[s]);
+              commit(&ofull[s]);
             }
           }
-          if (more) {
-            next();
-          }
+          if (more) next();
         }
-        umma_commit(qempty);
-        ++nq;
       }
-      ok = __shfl_sync(~0u, ok, 0);
-    }
-  } else if (warp < 4) {
-    if (blockIdx.x == 0 && warp == 2) report_bad_seqs(a, lane, 32);
-    const int tid = threadIdx.x - 64;
-    const int chunks = ksteps * 2, dchunks = a.dim / 8;
-    int nq = 0, nfix = 0;
-    long long it = 0;   // ring position of the tile's first block
-    bool ok = true;
-    for (long long id = blockIdx.x; walk.at(a, tile_rows, id, t) && ok; id += gridDim.x) {
-      if (t.blocks == 0) continue;
-      ok = op_wait_warp(qempty, (nq & 1) ^ 1u, &s_abort);
-      if (!ok) break;
-      ++nq;
-      const int rows = t.rows > kAtBM ? 2 * kAtBM : kAtBM;
-      // 16 threads (chunks of 8 values) a row
-      for (int i = tid >> 4; i < rows; i += 4) {
-        const int c = tid & 15;
-        const int r = t.r0 + i, pos = r / group, head = t.kvh * group + r - pos * group;
-        const bool there = i < t.rows && c < dchunks;
-        if (c < chunks)
-          cp_async16(sQ + (i >> 7) * Cfg::TILE + (c >> 3) * Cfg::BOX + (i & 127) * 128 + (((c & 7) ^ (i & 7)) << 4),
-                     there ? a.q + (t.s.q0 + pos) * a.q_t + head * a.q_h + c * 8 : a.q, there);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(qfull);
-      const int keys = t.end - (t.blocks - 1) * kAtBN;
-      if (warp == 3 && (keys & 15)) {
-        const long long p = it + 2 * t.blocks - 1;
-        ok = op_wait_warp(vgo, nfix++ & 1, &s_abort) &&
-             op_wait_warp(&full[p % SLOTS], (uint32_t)(p / SLOTS) & 1u, &s_abort);
-        if (!ok) break;
-        uint8_t* v = sKV + (p % SLOTS) * Cfg::TILE;
-        for (int i = lane; i < (16 - (keys & 15)) * (DP / 8); i += 32) {
-          const int row = keys + i / (DP / 8), c = i % (DP / 8);
-          *reinterpret_cast<uint4*>(v + (c >> 3) * Cfg::BOX + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vfix);
-      }
-      it += 2 * t.blocks;
+    } else if (warp == 2 && blockIdx.x == 0) {
+      report_bad_seqs(a, lane, 32);
     }
   } else {
+    set_max_regs_inc<kAtRegsSoftmax>();
+    walk.start<KEYS>(a, tile_pos);
     const int s = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
+    const int row_pos = row / group, row_head = row - row_pos * group;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + s * kAtBN, tO = tmem + lanes + 2 * kAtBN + s * 128;
     const float c = fabsf(a.scale_log2);
-    uint32_t sphase = 0, ophase = 0;
-    bool ok = true;
-    for (long long id = blockIdx.x; walk.at(a, tile_rows, id, t) && ok; id += gridDim.x) {
-      if (s * kAtBM >= t.rows) continue;
-      const int r = t.r0 + s * kAtBM + row;
-      const int pos = r / group;
-      const bool valid = s * kAtBM + row < t.rows;
-      int limit = valid ? t.s.nk : 0;   // keys that this row sees
+    const uint64_t c2 = f2_splat(c);
+    uint32_t sphase = 0, ophase = 0, tphase = 0;
+    for (long long round = 0;
+         walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
+      const int first_pos = KEYS ? 0 : s * half_pos;   // of this half in the tile
+      if (first_pos >= t.np) continue;
+      const int pos = t.p0 + first_pos + row_pos;
+      const bool valid = row_pos < half_pos && first_pos + row_pos < t.np;
+      const bool active = __any_sync(~0u, valid);      // a warp without rows only keeps the tensor core going
+      int limit = valid ? t.s.nk : 0;                  // keys that this row sees
       if (a.causal && valid) limit = max(0, min(limit, pos + t.s.nk - t.s.nq + 1));
       float top = -INFINITY, sum = 0.f;
-      for (int j = 0; j < t.blocks; ++j) {
+      int done = 0;                                    // blocks of this half
+      for (int j = KEYS ? s : 0; j < t.nb; j += KEYS ? 2 : 1, ++done) {
         ok = op_wait_warp(&sfull[s], sphase, &s_abort);
         if (!ok) break;
         sphase ^= 1u;
+        if (!active) {
+          if (lane == 0) mbar_arrive(&pfull[2 * s]), mbar_arrive(&pfull[2 * s + 1]);
+          __syncwarp();
+          continue;
+        }
         tc_fence_after();
         float v[128];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32(tS + x * 32, reinterpret_cast<uint32_t(&)[32]>(v[x * 32]));
         tmem_ld_wait();
-        const int left = limit - j * kAtBN;   // columns of this block that the row sees
+        const int left = limit - (t.b0 + j) * kAtBN;   // columns of this block that the row sees
         if (!__all_sync(~0u, left >= kAtBN)) {
 #pragma unroll
           for (int x = 0; x < 128; ++x) v[x] = x < left ? v[x] : -INFINITY;
         }
-        float m = v[0];
+        float m4[4] = {top, v[0], v[1], v[2]};
 #pragma unroll
-        for (int x = 1; x < 128; ++x) m = fmaxf(m, v[x]);
-        m = fmaxf(m, top);
+        for (int x = 3; x + 1 < 128; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
+        const float m = fmaxf(max3(m4[0], m4[1], m4[2]), fmaxf(m4[3], v[127]));
         // (an infinite difference included: the first block, or a row that saw nothing so far)
         if (__any_sync(~0u, (m - top) * c > 8.f)) {
           const float f = top == -INFINITY ? 0.f : ex2((top - m) * c);
-          if (j > 0) {
+          if (done > 0) {
 #pragma unroll 1
             for (int x = 0; x < a.dim; x += 32) {
               uint32_t o[32];
@@ -426,92 +498,217 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           sum *= f;
           top = m;
         }
-        const float base = top == -INFINITY ? 0.f : -top * c;
+        const uint64_t base2 = f2_splat(top == -INFINITY ? 0.f : -top * c);
+        uint64_t sums[2] = {f2_pack(sum, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 16; ++y) {
-            const float p0 = ex2(fmaf(v[x * 32 + 2 * y], c, base)), p1 = ex2(fmaf(v[x * 32 + 2 * y + 1], c, base));
-            sum += p0;
-            sum += p1;
-            p[y] = pack_bf16x2(p0, p1);
+            float e0, e1;
+            f2_unpack(f2_fma(f2_pack(v[x * 32 + 2 * y], v[x * 32 + 2 * y + 1]), c2, base2), e0, e1);
+            e0 = ex2(e0), e1 = ex2(e1);
+            sums[y & 1] = f2_add(sums[y & 1], f2_pack(e0, e1));
+            p[y] = pack_bf16x2(e0, e1);
           }
           tmem_st16(tS + x * 16, p);
+          if (x & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[2 * s + (x >> 1)]);
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[s]);
+        float s0, s1;
+        f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
+        sum = s0 + s1;
       }
       if (!ok) break;
-      if (t.blocks > 0) {
+      if (done > 0) {
         ok = op_wait_warp(&ofull[s], ophase, &s_abort);
         if (!ok) break;
         ophase ^= 1u;
         tc_fence_after();
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int head = t.kvh * group + r - pos * group;
-      __nv_bfloat16* orow = a.out + (t.s.q0 + pos) * a.o_t + head * a.o_h;
+      if constexpr (!KEYS) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int head = t.kvh * group + row_head;
+        __nv_bfloat16* orow = a.out + (t.s.q0 + pos) * a.o_t + head * a.o_h;
+        if (active) {
 #pragma unroll 1
-      for (int x = 0; x < a.dim; x += 32) {
-        float v[32] = {};
-        if (t.blocks > 0) {
-          tmem_ld32(tO + x, reinterpret_cast<uint32_t(&)[32]>(v));
-          tmem_ld_wait();
-        }
+          for (int x = 0; x < a.dim; x += 32) {
+            float v[32] = {};
+            if (done > 0) {
+              tmem_ld32(tO + x, reinterpret_cast<uint32_t(&)[32]>(v));
+              tmem_ld_wait();
+            }
 #pragma unroll
-        for (int y = 0; y < 32; ++y) v[y] = sum == 0.f ? 0.f : v[y] * inv;
-        if (valid) store_out_row(orow, out_vec, x, a.dim, v);
+            for (int y = 0; y < 32; ++y) v[y] = sum == 0.f ? 0.f : v[y] * inv;
+            if (valid) store_out_row(orow, out_mode, x, a.dim, v);
+          }
+        }
+        if (valid && a.lse != nullptr)
+          a.lse[(t.s.q0 + pos) * (long long)a.heads + head] =
+              sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.69314718055994531f;
+        tc_fence_before();   // these reads of O come before what the next tile's first block lets the tensor core write
+      } else {
+        // join: half 1 puts its output into `part`, half 0 adds its own, then every CTA adds up all parts of some of the rows
+        ok = op_wait_warp_cluster(jempty, tphase ^ 1u, &s_abort);
+        if (ok && s == 0) ok = op_wait_warp(hfull, tphase, &s_abort);
+        if (!ok) break;
+        if (active) {
+          float own = 1.f, other = 0.f;
+          if (s == 0) {
+            const float2 st = stats[row];
+            const float m = fmaxf(top, st.x);
+            own = top == -INFINITY ? 0.f : ex2((top - m) * c);
+            other = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
+            top = m;
+            sum = sum * own + st.y * other;
+          }
+#pragma unroll 1
+          for (int x = 0; x < a.dim; x += 32) {
+            float v[32] = {};
+            if (done > 0) {
+              tmem_ld32(tO + x, reinterpret_cast<uint32_t(&)[32]>(v));
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) {   // 16-byte pieces of a row in an order of its own: no bank conflicts
+              float4* p = reinterpret_cast<float4*>(part + row * DP) + (((x + y) >> 2) ^ (row & 7));
+              float4 o = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+              if (s == 0) {
+                const float4 h = *p;
+                // a half without keys counts nothing, whatever it holds
+                o.x = own == 0.f ? 0.f : o.x * own, o.y = own == 0.f ? 0.f : o.y * own;
+                o.z = own == 0.f ? 0.f : o.z * own, o.w = own == 0.f ? 0.f : o.w * own;
+                if (other != 0.f)
+                  o.x = fmaf(h.x, other, o.x), o.y = fmaf(h.y, other, o.y), o.z = fmaf(h.z, other, o.z),
+                  o.w = fmaf(h.w, other, o.w);
+              }
+              *p = o;
+            }
+          }
+          stats[row] = make_float2(top, sum);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (s == 1) mbar_arrive(hfull);
+          else
+            for (int r = 0; r < splits; ++r) mbar_arrive_cluster(mapa_shared(jfull, r));
+        }
+        ok = op_wait_warp_cluster(jfull, tphase, &s_abort);
+        if (!ok) break;
+        const int rows = t.np * group;
+        for (int i = rank + splits * (warp - 4); i < rows; i += splits * 8) {
+          float2 st[8];
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            if (r < splits) st[r] = ld_cluster_f2(mapa_shared(stats + i, r));
+            else st[r] = make_float2(-INFINITY, 0.f);
+            m = fmaxf(m, st[r].x);
+          }
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          const uint32_t at = (uint32_t)(i * DP * 4 + ((lane ^ (i & 7)) << 4));
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            if (st[r].x == -INFINITY) continue;
+            const float f = ex2((st[r].x - m) * c);
+            l = fmaf(st[r].y, f, l);
+            if (lane * 4 < DP) {
+              const float4 h = ld_cluster_f4(mapa_shared(part, r) + at);
+              o.x = fmaf(h.x, f, o.x), o.y = fmaf(h.y, f, o.y), o.z = fmaf(h.z, f, o.z), o.w = fmaf(h.w, f, o.w);
+            }
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int ip = i / group, head = t.kvh * group + i - ip * group;
+          const long long token = t.s.q0 + t.p0 + ip;
+          __nv_bfloat16* dst = a.out + token * a.o_t + head * a.o_h + lane * 4;
+          if (lane * 4 < a.dim) {
+            if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (out_mode > 0) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            } else {
+              dst[0] = __float2bfloat16_rn(o.x * inv), dst[1] = __float2bfloat16_rn(o.y * inv);
+              dst[2] = __float2bfloat16_rn(o.z * inv), dst[3] = __float2bfloat16_rn(o.w * inv);
+            }
+          }
+          if (lane == 0 && a.lse != nullptr)
+            a.lse[token * a.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+        }
+        __syncwarp();
+        if (lane == 0)
+          for (int r = 0; r < splits; ++r) mbar_arrive_cluster(mapa_shared(jempty, r));
+        tphase ^= 1u;
       }
-      if (valid && a.lse != nullptr)
-        a.lse[(t.s.q0 + pos) * (long long)a.heads + head] =
-            sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.69314718055994531f;
-      tc_fence_before();   // these reads of O come before what the next tile's first block lets the tensor core write
     }
   }
   __syncthreads();
+  if (KEYS && splits > 1) cluster_sync();   // nobody leaves while its part is read or its barriers are signalled
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-// [tokens][kv_heads][dim] bf16 with the given strides, boxes of 128 tokens x 1
-// head x 64 values, zeros past dim and past the last token.
+// [tokens][heads][dim] bf16 with the given strides, boxes of `box_tokens`
+// tokens x `box_heads` heads x 64 values, zeros past dim and past the last token.
 inline CUtensorMap make_heads_tmap(const __nv_bfloat16* p, long long tokens, int heads, int dim, long long st,
-                                   long long sh) {
+                                   long long sh, int box_tokens, int box_heads) {
   CUtensorMap m;
   cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
   cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
-  cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kAtBN};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   CUresult r = encode_fn()(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) throw GditError(GDIT_ECUDA, fmt("cuTensorMapEncodeTiled (keys) failed (%d)", (int)r));
+  if (r != CUDA_SUCCESS) throw GditError(GDIT_ECUDA, fmt("cuTensorMapEncodeTiled (heads) failed (%d)", (int)r));
   return m;
 }
 
-template <int DP>
-void launch_attention_tc(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int sms, int out_vec,
-                         cudaStream_t s) {
-  using Cfg = AttnCfg<DP>;
-  allow_smem(attention_tc_kernel<DP>, Cfg::SMEM);
-  launch_op(s, 1, attention_tc_kernel<DP>, dim3((unsigned)std::min<long long>(a.max_tiles * a.kv_heads, sms)),
-            dim3(kAtThreads), Cfg::SMEM, mk, mv, a, 2 * kAtBM, out_vec);
+template <int DP, bool KEYS>
+void launch_attention_as(const AttnArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                         int splits, int sms, int out_mode, cudaStream_t s) {
+  using Cfg = AttnCfg<DP, KEYS>;
+  auto kern = attention_kernel<DP, KEYS>;
+  allow_smem(kern, Cfg::SMEM, kAtRegs);
+  const int most = splits > 1 ? max_clusters(kern, splits, kAtThreads, Cfg::SMEM) : sms;
+  const int workers = (int)std::min<long long>(a.max_tiles * a.kv_heads, most);
+  launch_op(s, splits, kern, dim3((unsigned)(workers * splits)), dim3(kAtThreads), Cfg::SMEM, mq, mk, mv, a, splits,
+            out_mode);
 }
 
 inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
-  a.max_tiles = a.total_q * (a.heads / a.kv_heads) / (2 * kAtBM) + a.batch;
+  const int group = a.heads / a.kv_heads, half_pos = kAtBM / group;
+  // tiles of `pos` positions that the sequences can have at most
+  auto tiles = [&](int pos) { return std::min(a.total_q, a.total_q / pos + a.batch); };
+  // Rows that fill no second half, or too few tiles for the SMs: the halves,
+  // and the CTAs of a cluster, take parts of the keys instead.
+  const bool keys = a.max_q <= half_pos || tiles(2 * half_pos) * a.kv_heads * 2 <= sms;
+  a.max_tiles = tiles(keys ? half_pos : 2 * half_pos);
+  int splits = 1;
+  if (keys) {
+    const int blocks = a.max_k / kAtBN;
+    while (splits < 8 && blocks >= 4 * splits && a.max_tiles * a.kv_heads * splits < 4ll * sms) splits *= 2;
+  }
+  const CUtensorMap mq = make_heads_tmap(a.q, a.total_q, a.heads, a.dim, a.q_t, a.q_h, half_pos, group);
   const bool none = a.total_k == 0;   // no key: the maps are not used, but they have to be valid
-  const CUtensorMap mk = none ? make_heads_tmap(a.q, 1, 1, a.dim, a.dim, a.dim)
-                              : make_heads_tmap(a.k, a.total_k, a.kv_heads, a.dim, a.k_t, a.k_h);
-  const CUtensorMap mv = none ? mk : make_heads_tmap(a.v, a.total_k, a.kv_heads, a.dim, a.v_t, a.v_h);
-  const int out_vec = ((uintptr_t)a.out & 15u) == 0 && a.o_t % 8 == 0 && a.o_h % 8 == 0;
-  if (a.dim > 64) launch_attention_tc<128>(a, mk, mv, sms, out_vec, s);
-  else launch_attention_tc<64>(a, mk, mv, sms, out_vec, s);
+  const CUtensorMap mk = none ? mq : make_heads_tmap(a.k, a.total_k, a.kv_heads, a.dim, a.k_t, a.k_h, kAtBN, 1);
+  const CUtensorMap mv = none ? mq : make_heads_tmap(a.v, a.total_k, a.kv_heads, a.dim, a.v_t, a.v_h, kAtBN, 1);
+  auto rows_aligned = [&](int bytes) {
+    return (uintptr_t)a.out % bytes == 0 && a.o_t * 2 % bytes == 0 && a.o_h * 2 % bytes == 0;
+  };
+  const int out_mode = rows_aligned(32) ? 2 : rows_aligned(16) ? 1 : 0;
+  if (a.dim > 64) {
+    if (keys) launch_attention_as<128, true>(a, mq, mk, mv, splits, sms, out_mode, s);
+    else launch_attention_as<128, false>(a, mq, mk, mv, splits, sms, out_mode, s);
+  } else {
+    if (keys) launch_attention_as<64, true>(a, mq, mk, mv, splits, sms, out_mode, s);
+    else launch_attention_as<64, false>(a, mq, mk, mv, splits, sms, out_mode, s);
+  }
 }
 
 }  // namespace gdit

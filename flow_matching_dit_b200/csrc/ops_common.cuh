@@ -2,8 +2,10 @@
 // and f32, and launches with programmatic dependent launch.
 #pragma once
 
+#include <map>
 #include <mutex>
 #include <set>
+#include <tuple>
 #include <utility>
 
 #include "host.cuh"
@@ -48,6 +50,44 @@ __device__ __forceinline__ bool op_wait_warp(uint64_t* bar, uint32_t parity, vol
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = op_wait(bar, parity, abort);
   return __shfl_sync(~0u, ok, 0) != 0;
+}
+
+// The same, every lane polling: no lane waits for another's answer to pass through a shuffle.
+__device__ __forceinline__ bool op_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(~0u, op_wait(bar, parity, abort));
+}
+
+// The same for a barrier that other CTAs of the cluster arrive at: what they
+// wrote to shared memory before is visible then.
+__device__ __forceinline__ bool op_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool ok = op_wait_warp(bar, parity, abort);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Register split of a kernel's warpgroups: all four warps of one execute it.
+template <int N>
+__device__ __forceinline__ void set_max_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // 32 lanes x 32 (16) consecutive 32-bit TMEM columns, thread i of the warp lane base + i.
@@ -118,17 +158,51 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr int kMaxDevices = 64;
 
 // Lets a kernel have `bytes` of dynamic shared memory on the current device:
-// asked of the runtime once per kernel and device.
+// asked of the runtime once per kernel and device.  regs > 0: the registers of
+// a thread at launch that the kernel's setmaxnreg split adds up to.
 template <typename... KArgs>
-void allow_smem(void (*kern)(KArgs...), int bytes) {
+void allow_smem(void (*kern)(KArgs...), int bytes, int regs = 0) {
   static std::mutex mu;
   static std::set<std::pair<const void*, int>> done;
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
   std::lock_guard<std::mutex> lock(mu);
   if (done.count({(const void*)kern, dev})) return;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+    if (fa.numRegs != regs) throw GditError(GDIT_ECUDA, fmt("kernel built with %d registers a thread, not %d", fa.numRegs, regs));
+  }
   CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   done.insert({(const void*)kern, dev});
+}
+
+// Clusters of `size` CTAs of a kernel that the current device holds at a time.
+template <typename... KArgs>
+int max_clusters(void (*kern)(KArgs...), int size, int threads, int smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int>, int> known;
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[{(const void*)kern, dev, size}];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int most = 0;
+    CUDA_TRY(cudaOccupancyMaxActiveClusters(&most, kern, &cfg));
+    if (most < 1) throw GditError(GDIT_ECUDA, fmt("clusters of %d CTAs do not fit the device", size));
+    n = most;
+  }
+  return n;
 }
 
 // Every operator kernel starts with pdl_wait() before it touches memory, and
