@@ -342,30 +342,36 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       auto next = [&] {
         if (++slot == SLOTS) slot = 0, phase ^= 1u;
       };
-      auto commit = [&](uint64_t* bar) {
-        if (lane == 0) umma_commit(bar);
-        __syncwarp();
+      const uint32_t acc = uniform(tmem), q0 = uniform(smem_u32(sQ)), kv0 = uniform(smem_u32(sKV));
+      const uint32_t bars = uniform(smem_u32(full));
+      auto commit = [&](uint32_t bar) {   // bar: address of a barrier
+        const uint32_t u = uniform(bar);
+        if (elect_one()) umma_commit_at(u);
       };
-      auto qk = [&](int s, int sl) {
-        if (lane == 0) {
-          const uint32_t q = smem_u32(sQ + (KEYS ? 0 : s * Cfg::TILE)), k = smem_u32(sKV + sl * Cfg::TILE);
-          for (int x = 0; x < ksteps; ++x) {
-            const uint32_t o = (x >> 2) * Cfg::BOX + (x & 3) * 32;
-            umma_bf16(tmem + s * kAtBN, smem_desc_sw128(q + o), smem_desc_sw128(k + o), idesc_qk, x > 0);
+      auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
+      auto qk = [&](uint32_t s, int sl) {
+        const uint64_t q = smem_desc_sw128(q0 + (KEYS ? 0 : s * Cfg::TILE));
+        const uint64_t k = smem_desc_sw128(kv0 + uniform(sl) * Cfg::TILE);
+        const uint32_t d = acc + s * kAtBN, bar = at(sfull) + s * 8;
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < DP / 16; ++x) {
+            const uint64_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
+            umma_bf16_if(x < ksteps, d, q + o, k + o, idesc_qk, x > 0);
           }
-          umma_commit(&sfull[s]);
+          umma_commit_at(bar);
         }
-        __syncwarp();
       };
-      // P V of half s over the steps [x0, x1) of 16 keys
-      auto pv = [&](int s, int sl, int x0, int x1, bool first) {
-        if (lane == 0) {
-          const uint32_t v = smem_u32(sKV + sl * Cfg::TILE);
-          for (int x = x0; x < x1; ++x)
-            umma_bf16_ts(tmem + 2 * kAtBN + s * 128, tmem + s * kAtBN + x * 8,
-                         smem_desc_mn_sw128(v + x * 2048, Cfg::BOX), idesc_pv, !first || x > 0);
+      // P V of half s over 4 of the block's steps of 16 keys, those below `steps`
+      auto pv = [&](uint32_t s, int sl, int x0, int steps, bool first) {
+        const uint64_t v = smem_desc_mn_sw128(kv0 + uniform(sl) * Cfg::TILE, Cfg::BOX) + (x0 * 2048 >> 4);
+        const uint32_t p = acc + s * kAtBN + x0 * 8, d = acc + 2 * kAtBN + s * 128;
+        const uint32_t n = uniform(steps), f = uniform(first);
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            umma_bf16_ts_if(x0 + x < n, d, p + x * 8, v + (x * 2048 >> 4), idesc_pv, !f || x0 + x > 0);
         }
-        __syncwarp();
       };
       // V of block j is there, and zero where its last 16 keys lie behind the tile's last one
       auto wait_v = [&](int sl, uint32_t ph, int keys) {
@@ -392,11 +398,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           ok = op_wait_all(&full[slot], phase, &s_abort);
           if (!ok) break;
           tc_fence_after();
-          for (int s = 0; s < halves; ++s) qk(KEYS ? j : s, slot);
-          commit(&empty[slot]);
+          for (int s = 0; s < halves; ++s) qk(uniform(KEYS ? j : s), slot);
+          commit(at(empty) + slot * 8);
           next();
         }
-        if (t.nb <= ahead) commit(qempty);
+        if (t.nb <= ahead) commit(at(qempty));
         for (int j = 0; j < t.nb && ok; ++j) {
           const int vslot = slot;
           const uint32_t vphase = phase;
@@ -404,30 +410,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           const bool more = j + ahead < t.nb;
           const int keys = min(kAtBN, t.end - (t.b0 + j) * kAtBN), steps = (keys + 15) / 16;
           for (int h = 0; h < halves && ok; ++h) {
-            const int s = KEYS ? j & 1 : h;
+            const uint32_t s = uniform(KEYS ? j & 1 : h);
             const bool first = j < (KEYS ? 2 : 1);
             if (h == 0) ok = wait_v(vslot, vphase, keys);
             ok = ok && op_wait_all(&pfull[2 * s], (pphase >> s) & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            pv(s, vslot, 0, min(4, steps), first);
+            pv(s, vslot, 0, steps, first);
             ok = op_wait_all(&pfull[2 * s + 1], (pphase >> s) & 1u, &s_abort);
             pphase ^= 1u << s;
             if (!ok) break;
             tc_fence_after();
             pv(s, vslot, 4, steps, first);
-            if (h == halves - 1) commit(&empty[vslot]);
+            if (h == halves - 1) commit(at(empty) + vslot * 8);
             if (more) {
               if (h == 0) ok = op_wait_all(&full[slot], phase, &s_abort);
               if (!ok) break;
               tc_fence_after();
               qk(s, slot);
               if (h == halves - 1) {
-                commit(&empty[slot]);
-                if (j + ahead == t.nb - 1) commit(qempty);   // Q has been used for the last time
+                commit(at(empty) + slot * 8);
+                if (j + ahead == t.nb - 1) commit(at(qempty));   // Q has been used for the last time
               }
             } else {
-              commit(&ofull[s]);
+              commit(at(ofull) + s * 8);
             }
           }
           if (more) next();
