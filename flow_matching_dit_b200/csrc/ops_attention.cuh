@@ -83,9 +83,9 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 constexpr int kAtBM = 128;       // rows of a half
 constexpr int kAtBN = 128;       // keys of a block
 constexpr int kAtThreads = 384;
-// Registers of a thread: 168 at launch (64512 in all), then 72 for the first
-// warpgroup and 216 for the softmax ones (the same 64512).
-constexpr int kAtRegs = 168, kAtRegsIssue = 72, kAtRegsSoftmax = 216;
+// Registers of a thread: 168 at launch (64512 in all), then 104 for the first
+// warpgroup and 200 for the softmax ones (the same 64512).
+constexpr int kAtRegs = 168, kAtRegsIssue = 104, kAtRegsSoftmax = 200;
 static_assert(3 * kAtRegs == kAtRegsIssue + 2 * kAtRegsSoftmax, "register split");
 
 template <int DP, bool KEYS>   // head_dim rounded up to 64 or 128
@@ -333,48 +333,45 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         ok = __shfl_sync(~0u, ok, 0);
       }
     } else if (warp == 1) {
+      // What the loops below depend on is kept where the compiler sees that it is the same in all lanes.
       walk.start<KEYS>(a, tile_pos);
       const uint32_t idesc_qk = idesc_bf16_f32(kAtBM, kAtBN) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);   // -Q for a negative scale
       const uint32_t idesc_pv = idesc_bf16_f32(kAtBM, (a.dim + 15) / 16 * 16) | (1u << 16);            // V: N-major
       const int ksteps = (a.dim + 15) / 16;
-      int slot = 0, nq = 0;
-      uint32_t phase = 0, pphase = 0;   // pphase: bit s for half s
+      const uint32_t acc = uniform(tmem), q0 = uniform(smem_u32(sQ)), kv0 = uniform(smem_u32(sKV));
+      const uint32_t bars = uniform(smem_u32(full));
+      auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
+      uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;   // pphase: bit s for half s
       auto next = [&] {
         if (++slot == SLOTS) slot = 0, phase ^= 1u;
       };
-      const uint32_t acc = uniform(tmem), q0 = uniform(smem_u32(sQ)), kv0 = uniform(smem_u32(sKV));
-      const uint32_t bars = uniform(smem_u32(full));
-      auto commit = [&](uint32_t bar) {   // bar: address of a barrier
-        const uint32_t u = uniform(bar);
-        if (elect_one()) umma_commit_at(u);
+      auto commit = [&](uint32_t bar) {
+        if (elect_one()) umma_commit_at(bar);
       };
-      auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
-      auto qk = [&](uint32_t s, int sl) {
+      auto qk = [&](uint32_t s, uint32_t sl) {
         const uint64_t q = smem_desc_sw128(q0 + (KEYS ? 0 : s * Cfg::TILE));
-        const uint64_t k = smem_desc_sw128(kv0 + uniform(sl) * Cfg::TILE);
-        const uint32_t d = acc + s * kAtBN, bar = at(sfull) + s * 8;
+        const uint64_t k = smem_desc_sw128(kv0 + sl * Cfg::TILE);
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < DP / 16; ++x) {
             const uint64_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
-            umma_bf16_if(x < ksteps, d, q + o, k + o, idesc_qk, x > 0);
+            umma_bf16_if(x < ksteps, acc + s * kAtBN, q + o, k + o, idesc_qk, x > 0);
           }
-          umma_commit_at(bar);
+          umma_commit_at(at(sfull) + s * 8);
         }
       };
       // P V of half s over 4 of the block's steps of 16 keys, those below `steps`
-      auto pv = [&](uint32_t s, int sl, int x0, int steps, bool first) {
-        const uint64_t v = smem_desc_mn_sw128(kv0 + uniform(sl) * Cfg::TILE, Cfg::BOX) + (x0 * 2048 >> 4);
-        const uint32_t p = acc + s * kAtBN + x0 * 8, d = acc + 2 * kAtBN + s * 128;
-        const uint32_t n = uniform(steps), f = uniform(first);
+      auto pv = [&](uint32_t s, uint32_t sl, int x0, int steps, bool first) {
+        const uint64_t v = smem_desc_mn_sw128(kv0 + sl * Cfg::TILE, Cfg::BOX) + (x0 * 2048 >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            umma_bf16_ts_if(x0 + x < n, d, p + x * 8, v + (x * 2048 >> 4), idesc_pv, !f || x0 + x > 0);
+            umma_bf16_ts_if(x0 + x < steps, acc + 2 * kAtBN + s * 128, acc + s * kAtBN + (x0 + x) * 8, v + (x * 2048 >> 4),
+                            idesc_pv, !first || x0 + x > 0);
         }
       };
       // V of block j is there, and zero where its last 16 keys lie behind the tile's last one
-      auto wait_v = [&](int sl, uint32_t ph, int keys) {
+      auto wait_v = [&](uint32_t sl, uint32_t ph, int keys) {
         if (!op_wait_all(&full[sl], ph, &s_abort)) return false;
         if (keys & 15) {
           uint8_t* v = sKV + sl * Cfg::TILE;
@@ -389,52 +386,59 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       };
       for (long long round = 0;
            ok && walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
-        if (t.nb == 0) continue;
-        const int halves = !KEYS && t.np > half_pos ? 2 : 1;   // that share each block
-        ok = op_wait_all(qfull, nq & 1, &s_abort);
-        ++nq;
-        const int ahead = KEYS ? min(2, t.nb) : 1;
-        for (int j = 0; j < ahead && ok; ++j) {
-          ok = op_wait_all(&full[slot], phase, &s_abort);
+        const int nb = (int)uniform(t.nb), last_keys = (int)uniform(t.end - (t.b0 + t.nb - 1) * kAtBN);
+        const bool two = !KEYS && uniform(t.np > half_pos) != 0;   // both halves share each block
+        if (nb == 0) continue;
+        constexpr int AHEAD = KEYS ? 2 : 1;                        // blocks whose scores are asked for in advance
+        ok = op_wait_all(qfull, qphase, &s_abort);
+        qphase ^= 1u;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (j >= nb) break;
+          ok = ok && op_wait_all(&full[slot], phase, &s_abort);
           if (!ok) break;
           tc_fence_after();
-          for (int s = 0; s < halves; ++s) qk(uniform(KEYS ? j : s), slot);
+          qk(KEYS ? j : 0, slot);
+          if (two) qk(1, slot);
           commit(at(empty) + slot * 8);
           next();
         }
-        if (t.nb <= ahead) commit(at(qempty));
-        for (int j = 0; j < t.nb && ok; ++j) {
-          const int vslot = slot;
-          const uint32_t vphase = phase;
+        if (nb <= AHEAD) commit(at(qempty));
+        for (int j = 0; j < nb && ok; ++j) {
+          const uint32_t vslot = slot, vphase = phase;
           next();
-          const bool more = j + ahead < t.nb;
-          const int keys = min(kAtBN, t.end - (t.b0 + j) * kAtBN), steps = (keys + 15) / 16;
-          for (int h = 0; h < halves && ok; ++h) {
-            const uint32_t s = uniform(KEYS ? j & 1 : h);
-            const bool first = j < (KEYS ? 2 : 1);
-            if (h == 0) ok = wait_v(vslot, vphase, keys);
-            ok = ok && op_wait_all(&pfull[2 * s], (pphase >> s) & 1u, &s_abort);
-            if (!ok) break;
+          const bool more = j + AHEAD < nb;
+          const int keys = j == nb - 1 ? min(kAtBN, last_keys) : kAtBN, steps = (keys + 15) / 16;
+          // one half's turn: P V of this block, then the scores of the next
+          auto turn = [&](uint32_t s, bool opens, bool closes) {
+            if (opens && !wait_v(vslot, vphase, keys)) return false;
+            if (!op_wait_all(&pfull[2 * s], (pphase >> s) & 1u, &s_abort)) return false;
             tc_fence_after();
-            pv(s, vslot, 0, steps, first);
-            ok = op_wait_all(&pfull[2 * s + 1], (pphase >> s) & 1u, &s_abort);
+            pv(s, vslot, 0, steps, j < AHEAD);
+            if (!op_wait_all(&pfull[2 * s + 1], (pphase >> s) & 1u, &s_abort)) return false;
             pphase ^= 1u << s;
-            if (!ok) break;
             tc_fence_after();
-            pv(s, vslot, 4, steps, first);
-            if (h == halves - 1) commit(at(empty) + vslot * 8);
+            pv(s, vslot, 4, steps, j < AHEAD);
             if (more) {
-              if (h == 0) ok = op_wait_all(&full[slot], phase, &s_abort);
-              if (!ok) break;
-              tc_fence_after();
+              if (opens && !op_wait_all(&full[slot], phase, &s_abort)) return false;
               qk(s, slot);
-              if (h == halves - 1) {
-                commit(at(empty) + slot * 8);
-                if (j + ahead == t.nb - 1) commit(at(qempty));   // Q has been used for the last time
-              }
             } else {
               commit(at(ofull) + s * 8);
             }
+            if (closes) {
+              commit(at(empty) + vslot * 8);
+              if (more) {
+                commit(at(empty) + slot * 8);
+                if (j + AHEAD == nb - 1) commit(at(qempty));   // Q has been used for the last time
+              }
+            }
+            return true;
+          };
+          if constexpr (KEYS) {
+            ok = turn(j & 1, true, true);
+          } else {
+            ok = turn(0, true, !two);
+            if (two && ok) ok = turn(1, false, true);
           }
           if (more) next();
         }
