@@ -73,16 +73,20 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 //   warp 1       tcgen05.mma: S = Q K^T (f32, TMEM), O += P V (P from TMEM); zeroes the rows of the last V tile that lie
 //                behind the tile's last key within 16, since 0 times what they hold may be NaN
 //   warp 2       reports bad sequences
-//   warps 4-11   softmax of one half each: thread = row; P (bf16) overwrites S; O is rescaled only when the running maximum
-//                has grown by more than 2^8 (the statistics refer to the maximum in use, so nothing is lost), and
-//                divided by the sum at the end
+//   warps 4-11   softmax of one half each: thread = row; O is rescaled only when the running maximum has grown by more than
+//                2^8 (the statistics refer to the maximum in use, so nothing is lost), and divided by the sum at the end
 //
-// The tensor core executes in issue order P V (j), Q K^T (next block) of one
-// half, then of the other, so a full S also says that O holds the blocks before.
+// TMEM is full with two outputs of 128 columns: 256 columns are left for two
+// times scores and probabilities.  The scores are a mailbox of 128 columns that
+// both halves use in turn, emptied into registers as soon as they are there, and
+// each half has 64 columns of P.  So the tensor core computes the next scores of
+// a half while it still exponentiates the previous ones (scores in place of P
+// would make the chain scores, softmax, P V of each half bound the kernel).
 
 constexpr int kAtBM = 128;       // rows of a half
 constexpr int kAtBN = 128;       // keys of a block
 constexpr int kAtThreads = 384;
+constexpr int kAtColS = 0, kAtColP = 128, kAtColO = 256;   // TMEM: S; P of the halves (64 columns each); O of the halves (128)
 // Registers of a thread: 168 at launch (64512 in all), then 104 for the first
 // warpgroup and 200 for the softmax ones (the same 64512).
 constexpr int kAtRegs = 168, kAtRegsIssue = 104, kAtRegsSoftmax = 200;
@@ -247,8 +251,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint64_t* qfull = empty + SLOTS;
   uint64_t* qempty = qfull + 1;
   uint64_t* sfull = qempty + 1;              // [2]
-  uint64_t* pfull = sfull + 2;               // [2][2]: the first and the other 64 keys of a block
-  uint64_t* ofull = pfull + 4;               // [2]
+  uint64_t* sfree = sfull + 2;               // the scores have been read
+  uint64_t* pfull = sfree + 1;               // [2]
+  uint64_t* ofull = pfull + 2;               // [2]: P V of a block is done
   uint64_t* hfull = ofull + 2;               // half 1's part is in shared memory
   uint64_t* jfull = hfull + 1;               // the parts of all CTAs are
   uint64_t* jempty = jfull + 1;              // and have been read by all
@@ -260,8 +265,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     for (int i = 0; i < SLOTS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&sfull[s], 1), mbar_init(&ofull[s], 1);
-    for (int s = 0; s < 4; ++s) mbar_init(&pfull[s], 4);
+    for (int s = 0; s < 2; ++s) mbar_init(&sfull[s], 1), mbar_init(&pfull[s], 4), mbar_init(&ofull[s], 1);
+    mbar_init(sfree, 4);
     mbar_init(hfull, 4);
     mbar_init(jfull, 4 * splits);
     mbar_init(jempty, 8 * splits);
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 tma_load_3d(sQ + s * Cfg::TILE + x * Cfg::BOX, &tmQ, qfull, x * 64, t.kvh * group,
                             t.s.q0 + t.p0 + s * half_pos);
           }
-          // the order of use: K of the first block (first two in the keys kernel), then V of a block and K of a later one in turn
-          const int ahead = KEYS ? min(2, t.nb) : 1, turns = 2 * (t.nb - ahead);
+          // the order of use: K of the first blocks, then V of a block and K of a later one in turn
+          const int ahead = min(KEYS ? 3 : 2, t.nb), turns = 2 * (t.nb - ahead);
           for (int i = 0; i < 2 * t.nb && ok; ++i) {
             const int u = i - ahead;
             const bool is_v = u >= 0 && (u >= turns || (u & 1) == 0);
@@ -341,106 +346,76 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const uint32_t acc = uniform(tmem), q0 = uniform(smem_u32(sQ)), kv0 = uniform(smem_u32(sKV));
       const uint32_t bars = uniform(smem_u32(full));
       auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
-      uint32_t slot = 0, phase = 0, qphase = 0, pphase = 0;   // pphase: bit s for half s
+      uint32_t slot = 0, phase = 0, qphase = 0, sphase = 1, pphase = 0;   // pphase: bit s for half s
       auto next = [&] {
         if (++slot == SLOTS) slot = 0, phase ^= 1u;
       };
-      auto commit = [&](uint32_t bar) {
-        if (elect_one()) umma_commit_at(bar);
-      };
-      auto qk = [&](uint32_t s, uint32_t sl) {
-        const uint64_t q = smem_desc_sw128(q0 + (KEYS ? 0 : s * Cfg::TILE));
-        const uint64_t k = smem_desc_sw128(kv0 + sl * Cfg::TILE);
-        if (elect_one()) {
-#pragma unroll
-          for (int x = 0; x < DP / 16; ++x) {
-            const uint64_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
-            umma_bf16_if(x < ksteps, acc + s * kAtBN, q + o, k + o, idesc_qk, x > 0);
-          }
-          umma_commit_at(at(sfull) + s * 8);
-        }
-      };
-      // P V of half s over 4 of the block's steps of 16 keys, those below `steps`
-      auto pv = [&](uint32_t s, uint32_t sl, int x0, int steps, bool first) {
-        const uint64_t v = smem_desc_mn_sw128(kv0 + sl * Cfg::TILE, Cfg::BOX) + (x0 * 2048 >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            umma_bf16_ts_if(x0 + x < steps, acc + 2 * kAtBN + s * 128, acc + s * kAtBN + (x0 + x) * 8, v + (x * 2048 >> 4),
-                            idesc_pv, !first || x0 + x > 0);
-        }
-      };
-      // V of block j is there, and zero where its last 16 keys lie behind the tile's last one
-      auto wait_v = [&](uint32_t sl, uint32_t ph, int keys) {
-        if (!op_wait_all(&full[sl], ph, &s_abort)) return false;
-        if (keys & 15) {
-          uint8_t* v = sKV + sl * Cfg::TILE;
-          for (int i = lane; i < (16 - (keys & 15)) * (DP / 8); i += 32) {
-            const int row = keys + i / (DP / 8), c = i % (DP / 8);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * Cfg::BOX + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        return true;
-      };
       for (long long round = 0;
-           ok && walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
-        const int nb = (int)uniform(t.nb), last_keys = (int)uniform(t.end - (t.b0 + t.nb - 1) * kAtBN);
+           walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
+        const int nb = (int)uniform(t.nb), last_keys = (int)uniform(min(kAtBN, t.end - (t.b0 + t.nb - 1) * kAtBN));
         const bool two = !KEYS && uniform(t.np > half_pos) != 0;   // both halves share each block
         if (nb == 0) continue;
-        constexpr int AHEAD = KEYS ? 2 : 1;                        // blocks whose scores are asked for in advance
-        ok = op_wait_all(qfull, qphase, &s_abort);
+        // items in the order of their scores: (block, half); P V of an item comes `lag` items later
+        const int items = two ? 2 * nb : nb, lag = KEYS || two ? 2 : 1;
+        op_wait_through(qfull, qphase, &s_abort);
         qphase ^= 1u;
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-          if (j >= nb) break;
-          ok = ok && op_wait_all(&full[slot], phase, &s_abort);
-          if (!ok) break;
-          tc_fence_after();
-          qk(KEYS ? j : 0, slot);
-          if (two) qk(1, slot);
-          commit(at(empty) + slot * 8);
-          next();
-        }
-        if (nb <= AHEAD) commit(at(qempty));
-        for (int j = 0; j < nb && ok; ++j) {
-          const uint32_t vslot = slot, vphase = phase;
-          next();
-          const bool more = j + AHEAD < nb;
-          const int keys = j == nb - 1 ? min(kAtBN, last_keys) : kAtBN, steps = (keys + 15) / 16;
-          // one half's turn: P V of this block, then the scores of the next
-          auto turn = [&](uint32_t s, bool opens, bool closes) {
-            if (opens && !wait_v(vslot, vphase, keys)) return false;
-            if (!op_wait_all(&pfull[2 * s], (pphase >> s) & 1u, &s_abort)) return false;
-            tc_fence_after();
-            pv(s, vslot, 0, steps, j < AHEAD);
-            if (!op_wait_all(&pfull[2 * s + 1], (pphase >> s) & 1u, &s_abort)) return false;
-            pphase ^= 1u << s;
-            tc_fence_after();
-            pv(s, vslot, 4, steps, j < AHEAD);
-            if (more) {
-              if (opens && !op_wait_all(&full[slot], phase, &s_abort)) return false;
-              qk(s, slot);
-            } else {
-              commit(at(ofull) + s * 8);
+        uint32_t kslot = 0, vslot = 0;
+        for (int i = 0; i < items + lag; ++i) {
+          if (i < items) {
+            const uint32_t s = KEYS || two ? i & 1 : 0;
+            if (!two || s == 0) {   // the first to use this block's keys
+              op_wait_through(&full[slot], phase, &s_abort);
+              kslot = slot;
+              next();
             }
-            if (closes) {
-              commit(at(empty) + vslot * 8);
-              if (more) {
-                commit(at(empty) + slot * 8);
-                if (j + AHEAD == nb - 1) commit(at(qempty));   // Q has been used for the last time
+            op_wait_through(sfree, sphase, &s_abort);
+            sphase ^= 1u;
+            tc_fence_after();
+            const uint64_t q = smem_desc_sw128(q0 + (KEYS ? 0 : s * Cfg::TILE));
+            const uint64_t k = smem_desc_sw128(kv0 + kslot * Cfg::TILE);
+            if (elect_one()) {
+#pragma unroll
+              for (int x = 0; x < DP / 16; ++x) {
+                const uint64_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
+                umma_bf16_if(x < ksteps, acc + kAtColS, q + o, k + o, idesc_qk, x > 0);
+              }
+              umma_commit_at(at(sfull) + s * 8);
+              if (!two || s == 1) umma_commit_at(at(empty) + kslot * 8);
+              if (i == items - 1) umma_commit_at(at(qempty));
+            }
+          }
+          if (i >= lag) {
+            const int n = i - lag, j = two ? n >> 1 : n;
+            const uint32_t s = KEYS || two ? n & 1 : 0;
+            const bool first = KEYS ? n < 2 : j == 0;
+            const int keys = j == nb - 1 ? last_keys : kAtBN, steps = (keys + 15) / 16;
+            if (!two || s == 0) {   // the first to use this block's values
+              op_wait_through(&full[slot], phase, &s_abort);
+              vslot = slot;
+              next();
+              if (keys & 15) {   // zeros where the last 16 keys lie behind the tile's last one
+                uint8_t* v = sKV + vslot * Cfg::TILE;
+                for (int e = lane; e < (16 - (keys & 15)) * (DP / 8); e += 32) {
+                  const int row = keys + e / (DP / 8), c = e % (DP / 8);
+                  *reinterpret_cast<uint4*>(v + (c >> 3) * Cfg::BOX + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
               }
             }
-            return true;
-          };
-          if constexpr (KEYS) {
-            ok = turn(j & 1, true, true);
-          } else {
-            ok = turn(0, true, !two);
-            if (two && ok) ok = turn(1, false, true);
+            op_wait_through(&pfull[s], (pphase >> s) & 1u, &s_abort);
+            pphase ^= 1u << s;
+            tc_fence_after();
+            const uint64_t v = smem_desc_mn_sw128(kv0 + vslot * Cfg::TILE, Cfg::BOX);
+            const uint32_t pcol = acc + kAtColP + s * 64, o = acc + kAtColO + s * 128;
+            if (elect_one()) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                umma_bf16_ts_if(x < steps, o, pcol + x * 8, v + (x * 2048 >> 4), idesc_pv, !first || x > 0);
+              umma_commit_at(at(ofull) + s * 8);
+              if (!two || s == 1) umma_commit_at(at(empty) + vslot * 8);
+            }
           }
-          if (more) next();
         }
       }
     } else if (warp == 2 && blockIdx.x == 0) {
@@ -453,7 +428,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const int row_pos = row / group, row_head = row - row_pos * group;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + s * kAtBN, tO = tmem + lanes + 2 * kAtBN + s * 128;
+    const uint32_t tS = tmem + lanes + kAtColS, tP = tmem + lanes + kAtColP + s * 64, tO = tmem + lanes + kAtColO + s * 128;
     const float c = fabsf(a.scale_log2);
     const uint64_t c2 = f2_splat(c);
     uint32_t sphase = 0, ophase = 0, tphase = 0;
@@ -472,8 +447,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         ok = op_wait_warp(&sfull[s], sphase, &s_abort);
         if (!ok) break;
         sphase ^= 1u;
+        // the P V of this half's previous block: it has read P and written O
+        auto wait_o = [&] {
+          if (done > 0) {
+            ok = op_wait_warp(&ofull[s], ophase, &s_abort);
+            ophase ^= 1u;
+          }
+          return ok;
+        };
         if (!active) {
-          if (lane == 0) mbar_arrive(&pfull[2 * s]), mbar_arrive(&pfull[2 * s + 1]);
+          if (!wait_o()) break;
+          if (lane == 0) mbar_arrive(sfree), mbar_arrive(&pfull[s]);
           __syncwarp();
           continue;
         }
@@ -482,6 +466,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32(tS + x * 32, reinterpret_cast<uint32_t(&)[32]>(v[x * 32]));
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfree);
         const int left = limit - (t.b0 + j) * kAtBN;   // columns of this block that the row sees
         if (!__all_sync(~0u, left >= kAtBN)) {
 #pragma unroll
@@ -491,6 +478,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
         for (int x = 3; x + 1 < 128; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
         const float m = fmaxf(max3(m4[0], m4[1], m4[2]), fmaxf(m4[3], v[127]));
+        if (!wait_o()) break;
+        tc_fence_after();
         // (an infinite difference included: the first block, or a row that saw nothing so far)
         if (__any_sync(~0u, (m - top) * c > 8.f)) {
           const float f = top == -INFINITY ? 0.f : ex2((top - m) * c);
@@ -521,14 +510,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             sums[y & 1] = f2_add(sums[y & 1], f2_pack(e0, e1));
             p[y] = pack_bf16x2(e0, e1);
           }
-          tmem_st16(tS + x * 16, p);
-          if (x & 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[2 * s + (x >> 1)]);
-          }
+          tmem_st16(tP + x * 16, p);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[s]);
         float s0, s1;
         f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
         sum = s0 + s1;

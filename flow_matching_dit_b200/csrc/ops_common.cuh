@@ -52,9 +52,11 @@ __device__ __forceinline__ bool op_wait_warp(uint64_t* bar, uint32_t parity, vol
   return __shfl_sync(~0u, ok, 0) != 0;
 }
 
-// The same, every lane polling: no lane waits for another's answer to pass through a shuffle.
-__device__ __forceinline__ bool op_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(~0u, op_wait(bar, parity, abort));
+// The same for warps whose control flow should not depend on the outcome: every
+// lane polls, and after a wait has run out every wait returns at once, so that the
+// loops run to their end (on whatever the buffers hold).
+__device__ __forceinline__ void op_wait_through(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__builtin_expect(!mbar_try_wait(bar, parity), 0)) op_wait(bar, parity, abort);
 }
 
 // The same for a barrier that other CTAs of the cluster arrive at: what they
