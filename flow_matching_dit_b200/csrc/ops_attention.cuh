@@ -69,10 +69,11 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 //                               cluster take a part of the keys each: single tokens and too few tiles for the SMs.  The
 //                               partial outputs are joined in the order of the parts, through distributed shared memory.
 //
-//   warp 0       Q boxes, K and V tiles of 128 keys by TMA; K and V in a ring of SLOTS tiles in the order of their use
-//   warp 1       tcgen05.mma: S = Q K^T (f32, TMEM), O += P V (P from TMEM); zeroes the rows of the last V tile that lie
-//                behind the tile's last key within 16, since 0 times what they hold may be NaN
-//   warp 2       reports bad sequences
+//   warp 0       Q boxes, K and V tiles of 128 keys by TMA, each kind into a ring of its own
+//   warp 1       tcgen05.mma: S = Q K^T (f32, TMEM)
+//   warp 2       tcgen05.mma: O += P V (P from TMEM); zeroes the rows of the last V tile that lie behind the tile's last key
+//                within 16, since 0 times what they hold may be NaN
+//   warp 3       reports bad sequences
 //   warps 4-11   softmax of one half each: thread = row; O is rescaled only when the running maximum has grown by more than
 //                2^8 (the statistics refer to the maximum in use, so nothing is lost), and divided by the sum at the end
 //
@@ -81,7 +82,10 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 // both halves use in turn, emptied into registers as soon as they are there, and
 // each half has 64 columns of P.  So the tensor core computes the next scores of
 // a half while it still exponentiates the previous ones (scores in place of P
-// would make the chain scores, softmax, P V of each half bound the kernel).
+// would make the chain scores, softmax, P V of each half bound the kernel).  A
+// warp's waits, its address arithmetic and the issue of eight multiplications take
+// longer than the tensor core needs for them (64 cycles each), so two warps share
+// the issuing.
 
 constexpr int kAtBM = 128;       // rows of a half
 constexpr int kAtBN = 128;       // keys of a block
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const AttnArgs a, int splits, int out_mode) {
   using Cfg = AttnCfg<DP, KEYS>;
-  constexpr int SLOTS = Cfg::SLOTS;
+  constexpr int SLOTS = Cfg::SLOTS, KS = (SLOTS + 1) / 2, VS = SLOTS / 2;   // ring of K tiles, ring of V tiles behind it
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int s_abort;
@@ -299,8 +303,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     set_max_regs_dec<kAtRegsIssue>();
     if (warp == 0) {
       walk.start<KEYS>(a, tile_pos);
-      int slot = 0, nq = 0;
-      uint32_t phase = 0;
+      int kslot = 0, vslot = 0, nq = 0;
+      uint32_t kphase = 0, vphase = 0;
       const int boxes = a.dim > 64 ? 2 : 1;
       for (long long round = 0;
            ok && walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
@@ -321,13 +325,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const int u = i - ahead;
             const bool is_v = u >= 0 && (u >= turns || (u & 1) == 0);
             const int j = u < 0 ? i : u >= turns ? t.nb - ahead + u - turns : (u & 1) ? ahead + (u >> 1) : u >> 1;
-            ok = op_wait(&empty[slot], phase ^ 1u, &s_abort);
+            const int slot = is_v ? KS + vslot : kslot;
+            ok = op_wait(&empty[slot], (is_v ? vphase : kphase) ^ 1u, &s_abort);
             if (!ok) break;
             mbar_arrive_expect_tx(&full[slot], boxes * Cfg::BOX);
             for (int x = 0; x < boxes; ++x)
               tma_load_3d(sKV + slot * Cfg::TILE + x * Cfg::BOX, is_v ? &tmV : &tmK, &full[slot], x * 64, t.kvh,
                           t.s.k0 + (t.b0 + j) * kAtBN);
-            if (++slot == SLOTS) slot = 0, phase ^= 1u;
+            if (is_v) {
+              if (++vslot == VS) vslot = 0, vphase ^= 1u;
+            } else {
+              if (++kslot == KS) kslot = 0, kphase ^= 1u;
+            }
           }
           if (!ok) {   // only after a wait has run out: the loads under way land before the CTA leaves
             for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) {
@@ -338,87 +347,112 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         ok = __shfl_sync(~0u, ok, 0);
       }
     } else if (warp == 1) {
-      // What the loops below depend on is kept where the compiler sees that it is the same in all lanes.
       walk.start<KEYS>(a, tile_pos);
-      const uint32_t idesc_qk = idesc_bf16_f32(kAtBM, kAtBN) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);   // -Q for a negative scale
-      const uint32_t idesc_pv = idesc_bf16_f32(kAtBM, (a.dim + 15) / 16 * 16) | (1u << 16);            // V: N-major
+      const uint32_t idesc = idesc_bf16_f32(kAtBM, kAtBN) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);   // -Q for a negative scale
       const int ksteps = (a.dim + 15) / 16;
-      const uint32_t acc = uniform(tmem), q0 = uniform(smem_u32(sQ)), kv0 = uniform(smem_u32(sKV));
-      const uint32_t bars = uniform(smem_u32(full));
+      const uint32_t d = uniform(tmem) + kAtColS, bars = uniform(smem_u32(full));
+      const uint32_t q0 = desc_lo_k(uniform(smem_u32(sQ))), k0 = desc_lo_k(uniform(smem_u32(sKV)));
       auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
-      uint32_t slot = 0, phase = 0, qphase = 0, sphase = 1, pphase = 0;   // pphase: bit s for half s
-      auto next = [&] {
-        if (++slot == SLOTS) slot = 0, phase ^= 1u;
-      };
+      uint32_t slot = 0, phase = 0, qphase = 0, sphase = 1;
       for (long long round = 0;
            walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
-        const int nb = (int)uniform(t.nb), last_keys = (int)uniform(min(kAtBN, t.end - (t.b0 + t.nb - 1) * kAtBN));
+        const int nb = (int)uniform(t.nb);
         const bool two = !KEYS && uniform(t.np > half_pos) != 0;   // both halves share each block
         if (nb == 0) continue;
-        // items in the order of their scores: (block, half); P V of an item comes `lag` items later
-        const int items = two ? 2 * nb : nb, lag = KEYS || two ? 2 : 1;
         op_wait_through(qfull, qphase, &s_abort);
         qphase ^= 1u;
-        uint32_t kslot = 0, vslot = 0;
-        for (int i = 0; i < items + lag; ++i) {
-          if (i < items) {
-            const uint32_t s = KEYS || two ? i & 1 : 0;
-            if (!two || s == 0) {   // the first to use this block's keys
-              op_wait_through(&full[slot], phase, &s_abort);
-              kslot = slot;
-              next();
-            }
+        for (int j = 0; j < nb; ++j) {
+          op_wait_through(&full[slot], phase, &s_abort);
+          const uint32_t k = k0 + slot * (Cfg::TILE >> 4);
+          auto scores = [&](uint32_t s, bool closes) {
             op_wait_through(sfree, sphase, &s_abort);
             sphase ^= 1u;
             tc_fence_after();
-            const uint64_t q = smem_desc_sw128(q0 + (KEYS ? 0 : s * Cfg::TILE));
-            const uint64_t k = smem_desc_sw128(kv0 + kslot * Cfg::TILE);
+            const uint32_t q = q0 + (KEYS ? 0 : s * (Cfg::TILE >> 4));
+            auto step = [&](int x) {
+              const uint32_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
+              umma_bf16_lo(d, q + o, k + o, idesc, x > 0);
+            };
             if (elect_one()) {
+              if (ksteps == DP / 16) {
 #pragma unroll
-              for (int x = 0; x < DP / 16; ++x) {
-                const uint64_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
-                umma_bf16_if(x < ksteps, acc + kAtColS, q + o, k + o, idesc_qk, x > 0);
+                for (int x = 0; x < DP / 16; ++x) step(x);
+              } else {
+#pragma unroll 1
+                for (int x = 0; x < ksteps; ++x) step(x);
               }
               umma_commit_at(at(sfull) + s * 8);
-              if (!two || s == 1) umma_commit_at(at(empty) + kslot * 8);
-              if (i == items - 1) umma_commit_at(at(qempty));
-            }
-          }
-          if (i >= lag) {
-            const int n = i - lag, j = two ? n >> 1 : n;
-            const uint32_t s = KEYS || two ? n & 1 : 0;
-            const bool first = KEYS ? n < 2 : j == 0;
-            const int keys = j == nb - 1 ? last_keys : kAtBN, steps = (keys + 15) / 16;
-            if (!two || s == 0) {   // the first to use this block's values
-              op_wait_through(&full[slot], phase, &s_abort);
-              vslot = slot;
-              next();
-              if (keys & 15) {   // zeros where the last 16 keys lie behind the tile's last one
-                uint8_t* v = sKV + vslot * Cfg::TILE;
-                for (int e = lane; e < (16 - (keys & 15)) * (DP / 8); e += 32) {
-                  const int row = keys + e / (DP / 8), c = e % (DP / 8);
-                  *reinterpret_cast<uint4*>(v + (c >> 3) * Cfg::BOX + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+              if (closes) {
+                umma_commit_at(at(empty) + slot * 8);
+                if (j == nb - 1) umma_commit_at(at(qempty));   // Q has been used for the last time
               }
             }
-            op_wait_through(&pfull[s], (pphase >> s) & 1u, &s_abort);
-            pphase ^= 1u << s;
-            tc_fence_after();
-            const uint64_t v = smem_desc_mn_sw128(kv0 + vslot * Cfg::TILE, Cfg::BOX);
-            const uint32_t pcol = acc + kAtColP + s * 64, o = acc + kAtColO + s * 128;
-            if (elect_one()) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                umma_bf16_ts_if(x < steps, o, pcol + x * 8, v + (x * 2048 >> 4), idesc_pv, !first || x > 0);
-              umma_commit_at(at(ofull) + s * 8);
-              if (!two || s == 1) umma_commit_at(at(empty) + vslot * 8);
-            }
+          };
+          if constexpr (KEYS) {
+            scores(j & 1, true);
+          } else {
+            scores(0, !two);
+            if (two) scores(1, true);
           }
+          if (++slot == KS) slot = 0, phase ^= 1u;
         }
       }
-    } else if (warp == 2 && blockIdx.x == 0) {
+    } else if (warp == 2) {
+      walk.start<KEYS>(a, tile_pos);
+      const uint32_t idesc = idesc_bf16_f32(kAtBM, (a.dim + 15) / 16 * 16) | (1u << 16);   // V: N-major
+      const uint32_t acc = uniform(tmem), bars = uniform(smem_u32(full));
+      const uint32_t v0 = desc_lo_mn(uniform(smem_u32(sKV)) + KS * Cfg::TILE, Cfg::BOX);
+      auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
+      uint32_t slot = 0, phase = 0, pphase[2] = {0, 0};
+      for (long long round = 0;
+           walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
+        const int nb = (int)uniform(t.nb), last_keys = (int)uniform(min(kAtBN, t.end - (t.b0 + t.nb - 1) * kAtBN));
+        const bool two = !KEYS && uniform(t.np > half_pos) != 0;
+        for (int j = 0; j < nb; ++j) {
+          op_wait_through(&full[KS + slot], phase, &s_abort);
+          const int keys = j == nb - 1 ? last_keys : kAtBN, steps = (keys + 15) / 16;
+          if (keys & 15) {   // zeros where the last 16 keys lie behind the tile's last one
+            uint8_t* v = sKV + (KS + slot) * Cfg::TILE;
+            for (int e = lane; e < (16 - (keys & 15)) * (DP / 8); e += 32) {
+              const int row = keys + e / (DP / 8), c = e % (DP / 8);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * Cfg::BOX + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          const uint32_t v = v0 + slot * (Cfg::TILE >> 4);
+          auto values = [&](uint32_t s, uint32_t& ph, bool closes) {
+            op_wait_through(&pfull[s], ph, &s_abort);
+            ph ^= 1u;
+            tc_fence_after();
+            const uint32_t p = acc + kAtColP + s * 64, o = acc + kAtColO + s * 128;
+            const bool first = KEYS ? j < 2 : j == 0;
+            auto step = [&](int x) {
+              umma_bf16_ts_lo(o, p + x * 8, v + (x * 2048 >> 4), idesc, x > 0 || !first);
+            };
+            if (elect_one()) {
+              if (steps == kAtBN / 16) {
+#pragma unroll
+                for (int x = 0; x < kAtBN / 16; ++x) step(x);
+              } else {
+#pragma unroll 1
+                for (int x = 0; x < steps; ++x) step(x);
+              }
+              umma_commit_at(at(ofull) + s * 8);
+              if (closes) umma_commit_at(at(empty) + (KS + slot) * 8);
+            }
+          };
+          if constexpr (KEYS) {
+            if (j & 1) values(1, pphase[1], true);
+            else values(0, pphase[0], true);
+          } else {
+            values(0, pphase[0], !two);
+            if (two) values(1, pphase[1], true);
+          }
+          if (++slot == VS) slot = 0, phase ^= 1u;
+        }
+      }
+    } else if (blockIdx.x == 0) {
       report_bad_seqs(a, lane, 32);
     }
   } else {
