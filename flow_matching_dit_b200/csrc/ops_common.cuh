@@ -28,6 +28,21 @@ __device__ __forceinline__ float4 bf16x4_to_f32(uint2 v) {
                      __uint_as_float(v.y & 0xffff0000u));
 }
 
+// Streamed once: not kept in L1, which the per-channel vectors use.
+__device__ __forceinline__ float4 load_f32x4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint2 load_b16x4(const __nv_bfloat16* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 // Waits for a phase of an mbarrier of this CTA; false once a wait of the CTA has
 // run out (2 s), which the status word then says.  *abort is in shared memory:
 // the CTA's other waits give up soon after, other calls are not concerned.

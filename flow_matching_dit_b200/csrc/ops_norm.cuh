@@ -2,6 +2,8 @@
 // u = pre(h') (1 + scale) + shift, one pass over the rows.
 #pragma once
 
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace gdit {
@@ -21,208 +23,166 @@ struct NormArgs {
   float residual_scale, eps;
 };
 
-// Mean and sum of squared deviations of n values, and their union (Chan,
-// Golub and LeVeque's pairwise update): no cancellation when the mean is large
-// against the deviations.
-struct Moments {
-  float n, mean, m2;
-};
-
-__device__ __forceinline__ Moments merge(Moments a, Moments b) {
-  const float n = a.n + b.n;
-  if (n == 0.f) return a;
-  const float d = b.mean - a.mean, f = b.n / n;
-  return {n, a.mean + d * f, a.m2 + b.m2 + d * d * a.n * f};
-}
-
-__device__ __forceinline__ float load_elt(const void* p, long long i, int f32) {
-  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ void store_elt(void* p, long long i, int f32, float v) {
-  if (f32) static_cast<float*>(p)[i] = v;
-  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
-// 8 consecutive values; i a multiple of 8 on 16-byte aligned rows.
-__device__ __forceinline__ void load8(const void* p, long long i, int f32, float (&v)[8]) {
-  if (f32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-    const float4 x = bf16x4_to_f32(make_uint2(a.x, a.y)), y = bf16x4_to_f32(make_uint2(a.z, a.w));
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-  }
-}
-
-__device__ __forceinline__ void store8(void* p, long long i, int f32, const float (&v)[8]) {
-  if (f32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
-  }
-}
-
-// One row is held by a team of `team` threads (whole warps), 8 * NV values a
-// thread, all in registers.  VEC: thread t holds the 8-value vectors t, t +
-// team, ...; otherwise the values t, t + team, ...
-template <bool VEC, int NV>
+// A row is held in registers by a team of whole warps, 4 * NU values a thread,
+// and read and written once; two rows of a warp are never in flight, other warps
+// hide its latency.  What bounds it: memory (h and y in, h' and u out).
+// A warp of the team takes 128 * NU neighbouring values, so that a thread's
+// addresses differ by constants:
+//   VEC   lane i holds the 4-value units i, i + 32, ...: 16 bytes of f32 or 8 of bf16
+//   else  the values i, i + 32, ...: any width and alignment
+// Mean and variance are sums over the registers, the second of squared deviations
+// from the first: no cancellation when the mean is large.
+template <bool VEC, int NU>
 struct RowTeam {
-  int dim, team, t, warps, bar;
-  float* red;   // 3 floats per warp of the team
+  static constexpr int N = 4 * NU;
+  int first, left;   // first value of this thread; values of the row from there on
+  int warp, warps, bar;
+  float* red;        // two times a float per warp of the team
+  int which;         // of the two, in turn
 
-  __device__ __forceinline__ int index(int c, int j) const {   // of value j of vector c
-    return VEC ? (c * team + t) * 8 + j : (c * 8 + j) * team + t;
+  __device__ __forceinline__ static constexpr int offset(int e) {   // of value e from the first
+    return VEC ? (e >> 2) * 128 + (e & 3) : e * 32;
+  }
+  __device__ __forceinline__ bool there(int e) const { return offset(e) < left; }
+
+  __device__ __forceinline__ void load(const void* p, long long base, int f32, float (&v)[N]) const {
+    if (VEC) {
+      if (f32) {
+        const float* q = static_cast<const float*>(p) + base + first;
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (there(c)) f = load_f32x4(q + offset(c));
+          v[c] = f.x, v[c + 1] = f.y, v[c + 2] = f.z, v[c + 3] = f.w;
+        }
+      } else {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + base + first;
+        uint2 w[NU];
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+          w[c >> 2] = make_uint2(0, 0);
+          if (there(c)) w[c >> 2] = load_b16x4(q + offset(c));
+        }
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+          const float4 f = bf16x4_to_f32(w[c >> 2]);
+          v[c] = f.x, v[c + 1] = f.y, v[c + 2] = f.z, v[c + 3] = f.w;
+        }
+      }
+    } else if (f32) {
+      const float* q = static_cast<const float*>(p) + base + first;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = there(e) ? q[offset(e)] : 0.f;
+    } else {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + base + first;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = there(e) ? __bfloat162float(q[offset(e)]) : 0.f;
+    }
   }
 
-  __device__ __forceinline__ void load(const void* p, long long base, int f32, float (&v)[NV][8]) const {
+  __device__ __forceinline__ void store(void* p, long long base, int f32, const float (&v)[N]) const {
+    if (f32) {
+      float* q = static_cast<float*>(p) + base + first;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      if (VEC) {
-        if (index(c, 0) < dim) load8(p, base + index(c, 0), f32, v[c]);
-      } else {
+      for (int e = 0; e < N; e += VEC ? 4 : 1) {
+        if (!there(e)) continue;
+        if (VEC) *reinterpret_cast<float4*>(q + offset(e)) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        else q[offset(e)] = v[e];
+      }
+    } else {
+      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + base + first;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (index(c, j) < dim) v[c][j] = load_elt(p, base + index(c, j), f32);
+      for (int e = 0; e < N; e += VEC ? 4 : 1) {
+        if (!there(e)) continue;
+        if (VEC) *reinterpret_cast<uint2*>(q + offset(e)) = make_uint2(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]));
+        else q[offset(e)] = __float2bfloat16_rn(v[e]);
       }
     }
   }
 
-  __device__ __forceinline__ void store(void* p, long long base, int f32, const float (&v)[NV][8]) const {
+  // v = v * (one + a) + b with per-channel f32 vectors (NULL: one = 0, a = 1; b = 0)
+  __device__ __forceinline__ void affine(float (&v)[N], const float* a, const float* b, float one) const {
+    if (a != nullptr) {
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      if (VEC) {
-        if (index(c, 0) < dim) store8(p, base + index(c, 0), f32, v[c]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (index(c, j) < dim) store_elt(p, base + index(c, j), f32, v[c][j]);
+      for (int e = 0; e < N; e += VEC ? 4 : 1) {
+        if (!there(e)) continue;
+        if (VEC) {
+          const float4 f = *reinterpret_cast<const float4*>(a + first + offset(e));
+          v[e] *= one + f.x, v[e + 1] *= one + f.y, v[e + 2] *= one + f.z, v[e + 3] *= one + f.w;
+        } else {
+          v[e] *= one + a[first + offset(e)];
+        }
       }
     }
-  }
-
-  // v = v * a + b with per-channel f32 vectors (NULL: 1 or 0; one: a is 1 + a)
-  __device__ __forceinline__ void affine(float (&v)[NV][8], const float* a, const float* b, float one) const {
-    if (a == nullptr && b == nullptr) return;
+    if (b != nullptr) {
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      if (VEC) {
-        if (index(c, 0) >= dim) continue;
-        float f[8];
-        if (a != nullptr) {
-          load8(a, index(c, 0), 1, f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] *= one + f[j];
-        }
-        if (b != nullptr) {
-          load8(b, index(c, 0), 1, f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] += f[j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (index(c, j) >= dim) continue;
-          if (a != nullptr) v[c][j] *= one + a[index(c, j)];
-          if (b != nullptr) v[c][j] += b[index(c, j)];
+      for (int e = 0; e < N; e += VEC ? 4 : 1) {
+        if (!there(e)) continue;
+        if (VEC) {
+          const float4 f = *reinterpret_cast<const float4*>(b + first + offset(e));
+          v[e] += f.x, v[e + 1] += f.y, v[e + 2] += f.z, v[e + 3] += f.w;
+        } else {
+          v[e] += b[first + offset(e)];
         }
       }
     }
   }
 
-  // The row's moments, in every thread of the team.
-  __device__ __forceinline__ Moments moments(const float (&v)[NV][8]) const {
-    float n = 0.f, sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (index(c, VEC ? 0 : j) < dim) n += 1.f, sum += v[c][j];
-    Moments m = {n, n > 0.f ? sum / n : 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (index(c, VEC ? 0 : j) < dim) m.m2 += (v[c][j] - m.mean) * (v[c][j] - m.mean);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Moments b = {__shfl_xor_sync(~0u, m.n, o), __shfl_xor_sync(~0u, m.mean, o),
-                         __shfl_xor_sync(~0u, m.m2, o)};
-      // the lower lane's moments first on both sides, so that both get the same bits
-      m = (threadIdx.x & o) ? merge(b, m) : merge(m, b);
-    }
-    if (warps > 1) {
-      const int w = t >> 5;
-      named_bar_sync(bar, team);   // the previous sums have been read
-      if ((t & 31) == 0) red[3 * w] = m.n, red[3 * w + 1] = m.mean, red[3 * w + 2] = m.m2;
-      named_bar_sync(bar, team);
-      m = {red[0], red[1], red[2]};
-      for (int i = 1; i < warps; ++i) m = merge(m, {red[3 * i], red[3 * i + 1], red[3 * i + 2]});
-    }
-    return m;
-  }
-
-  __device__ __forceinline__ float square_sum(const float (&v)[NV][8]) const {
-    float s = 0.f;
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (index(c, VEC ? 0 : j) < dim) s += v[c][j] * v[c][j];
+  // The team's sum, the same bits in every thread.
+  __device__ __forceinline__ float total(float s) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     if (warps > 1) {
-      named_bar_sync(bar, team);
-      if ((t & 31) == 0) red[t >> 5] = s;
-      named_bar_sync(bar, team);
-      s = red[0];
-      for (int i = 1; i < warps; ++i) s += red[i];
+      float* r = red + which * warps;
+      which ^= 1;   // so that one barrier is enough: the sum before last has been read
+      if ((threadIdx.x & 31) == 0) r[warp] = s;
+      named_bar_sync(bar, 32 * warps);
+      s = r[0];
+      for (int i = 1; i < warps; ++i) s += r[i];
     }
     return s;
   }
 
-  __device__ __forceinline__ void norm(float (&v)[NV][8], int kind, const float* gain, const float* bias,
-                                       float eps) const {
+  __device__ __forceinline__ void norm(float (&v)[N], int kind, const float* gain, const float* bias, float eps, float dim) {
     if (kind == GDIT_NORM_NONE) return;
-    float mean = 0.f, rs;
+    float mean = 0.f, s = 0.f;
     if (kind == GDIT_NORM_LAYER) {
-      const Moments m = moments(v);
-      mean = m.mean;
-      rs = rsqrtf(m.m2 / (float)dim + eps);
-    } else {
-      rs = rsqrtf(square_sum(v) / (float)dim + eps);
+#pragma unroll
+      for (int e = 0; e < N; ++e) s += v[e];   // 0 behind the row's end
+      mean = total(s) / dim;
+      s = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
+    for (int e = 0; e < N; ++e) {
+      v[e] -= mean;
+      if (there(e)) s = fmaf(v[e], v[e], s);
+    }
+    const float rs = rsqrtf(total(s) / dim + eps);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = (v[c][j] - mean) * rs;
+    for (int e = 0; e < N; ++e) v[e] *= rs;
     affine(v, gain, bias, 0.f);
   }
 };
 
 constexpr int kNormThreads = 512;   // most threads of a CTA
 
-template <bool VEC, int NV>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, int team, int teams) {
-  __shared__ float red[kNormThreads / 32 * 3];
-  const int which = threadIdx.x / team;
-  RowTeam<VEC, NV> T;
-  T.dim = a.dim;
-  T.team = team;
-  T.t = threadIdx.x - which * team;
-  T.warps = team >> 5;
+template <bool VEC, int NU>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, int warps, int teams) {
+  __shared__ float red[kNormThreads / 32 * 2];
+  const int which = threadIdx.x / (32 * warps);
+  RowTeam<VEC, NU> T;
+  T.warps = warps;
+  T.warp = (threadIdx.x >> 5) - which * warps;
+  T.first = T.warp * 128 * NU + (threadIdx.x & 31) * (VEC ? 4 : 1);
+  T.left = a.dim - T.first;
   T.bar = 1 + which;
-  T.red = red + which * T.warps * 3;
+  T.red = red + which * warps * 2;
+  T.which = 0;
+  const float dim = (float)a.dim;
   pdl_wait();
   pdl_launch_dependents();
   for (long long r = (long long)blockIdx.x * teams + which; r < a.rows; r += (long long)gridDim.x * teams) {
-    float h[NV][8], y[NV][8];
+    float h[4 * NU], y[4 * NU];
     T.load(a.h, r * a.ldh, a.h_f32, h);
     if (a.y != nullptr) T.load(a.y, r * a.ldy, a.y_f32, y);
     long long g = a.row_group != nullptr ? a.row_group[r] : 0;
@@ -231,23 +191,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, in
                                     (a.mod_groups > 1 && g >= a.mod_groups));
     if (bad) {
       g = 0;
-      if (T.t == 0) atomicOr(&g_op_status, OP_ERR_GROUP);
+      if (T.first == 0) atomicOr(&g_op_status, OP_ERR_GROUP);
     }
     const long long go = a.gate_groups > 1 ? g * a.dim : 0, mo = a.mod_groups > 1 ? g * a.dim : 0;
     if (a.y != nullptr) {
-      T.norm(y, a.post, a.post_gain, a.post_bias, a.eps);
+      T.norm(y, a.post, a.post_gain, a.post_bias, a.eps, dim);
       T.affine(y, a.gate != nullptr ? a.gate + go : nullptr, nullptr, 0.f);
     }
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[c][j] = a.y != nullptr ? fmaf(a.residual_scale, h[c][j], y[c][j]) : a.residual_scale * h[c][j];
-        if (bad) h[c][j] = __int_as_float(0x7fffffff);
-      }
+    for (int e = 0; e < 4 * NU; ++e) {
+      h[e] = a.y != nullptr ? fmaf(a.residual_scale, h[e], y[e]) : a.residual_scale * h[e];
+      if (!T.there(e)) h[e] = 0.f;
+      if (bad) h[e] = __int_as_float(0x7fffffff);
+    }
     if (a.out_h != nullptr) T.store(a.out_h, r * a.ldoh, a.h_f32, h);
     if (a.out_u != nullptr) {
-      T.norm(h, a.pre, a.pre_gain, a.pre_bias, a.eps);
+      T.norm(h, a.pre, a.pre_gain, a.pre_bias, a.eps, dim);
       T.affine(h, a.scale != nullptr ? a.scale + mo : nullptr, a.shift != nullptr ? a.shift + mo : nullptr, 1.f);
       T.store(a.out_u, r * a.ldou, a.u_f32, h);
     }
@@ -255,28 +214,32 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, in
 }
 
 inline void launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
-  auto aligned = [&](const void* p, long long ld, int f32) {
-    return p == nullptr || (((uintptr_t)p & 15u) == 0 && (ld * (f32 ? 4 : 2)) % 16 == 0);
+  auto aligned = [&](const void* p, long long ld, int f32) {   // units of 4 values
+    const int bytes = f32 ? 16 : 8;
+    return p == nullptr || ((uintptr_t)p % bytes == 0 && (ld * (f32 ? 4 : 2)) % bytes == 0);
   };
-  bool vec = a.dim % 8 == 0 && aligned(a.h, a.ldh, a.h_f32) && aligned(a.y, a.ldy, a.y_f32) &&
+  bool vec = a.dim % 4 == 0 && aligned(a.h, a.ldh, a.h_f32) && aligned(a.y, a.ldy, a.y_f32) &&
              aligned(a.out_h, a.ldoh, a.h_f32) && aligned(a.out_u, a.ldou, a.u_f32);
   for (const float* p : {a.post_gain, a.post_bias, a.gate, a.pre_gain, a.pre_bias, a.scale, a.shift})
     vec = vec && ((uintptr_t)p & 15u) == 0;
-  int nv = 1;
-  while (8 * nv * kNormThreads < a.dim) nv *= 2;
-  const int team = ((a.dim + 8 * nv - 1) / (8 * nv) + 31) / 32 * 32;
-  const int teams = std::max(1, 256 / team);
-  const long long blocks = std::min<long long>((a.rows + teams - 1) / teams, (long long)sms * 8);
-  const dim3 grid((unsigned)blocks), block(team * teams);
-  if (vec) {
-    if (nv == 1) launch_op(s, 1, norm_kernel<true, 1>, grid, block, 0, a, team, teams);
-    else if (nv == 2) launch_op(s, 1, norm_kernel<true, 2>, grid, block, 0, a, team, teams);
-    else launch_op(s, 1, norm_kernel<true, 4>, grid, block, 0, a, team, teams);
-  } else {
-    if (nv == 1) launch_op(s, 1, norm_kernel<false, 1>, grid, block, 0, a, team, teams);
-    else if (nv == 2) launch_op(s, 1, norm_kernel<false, 2>, grid, block, 0, a, team, teams);
-    else launch_op(s, 1, norm_kernel<false, 4>, grid, block, 0, a, team, teams);
-  }
+  // Warps of a row: as few as hold it with 32 values a thread, so that a row of
+  // up to 1024 needs no barrier; more where the rows leave the SMs without warps.
+  int warps = (a.dim + 1023) / 1024;
+  while (a.rows * warps < 8ll * sms && 128 * warps < a.dim && warps < 8) warps *= 2;
+  const int units = (a.dim + 128 * warps - 1) / (128 * warps);   // of 4 values a thread
+  const int teams = std::max(1, 8 / warps);
+  const dim3 grid((unsigned)std::min<long long>((a.rows + teams - 1) / teams, INT32_MAX)), block(32 * warps * teams);
+  auto launch = [&](auto kern) { launch_op(s, 1, kern, grid, block, 0, a, warps, teams); };
+  auto pick = [&](auto v) {
+    constexpr bool V = decltype(v)::value;
+    if (units == 1) launch(norm_kernel<V, 1>);
+    else if (units == 2) launch(norm_kernel<V, 2>);
+    else if (units <= 4) launch(norm_kernel<V, 4>);
+    else if (units <= 6) launch(norm_kernel<V, 6>);
+    else launch(norm_kernel<V, 8>);
+  };
+  if (vec) pick(std::true_type());
+  else pick(std::false_type());
 }
 
 }  // namespace gdit
