@@ -13,7 +13,8 @@ nothing but the outputs it returns and may be captured in a CUDA graph.
 
 from __future__ import annotations
 
-from ctypes import byref
+import ctypes
+import struct
 
 import torch
 
@@ -28,6 +29,39 @@ ACTIVATIONS = {None: GDIT_ACT_NONE, "none": GDIT_ACT_NONE, "relu": GDIT_ACT_RELU
 NORMS = {None: GDIT_NORM_NONE, "none": GDIT_NORM_NONE, "layer": GDIT_NORM_LAYER, "rms": GDIT_NORM_RMS}
 _DTYPE = {torch.float32: GDIT_F32, torch.bfloat16: GDIT_BF16}
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+
+
+class _Op:
+    """An entry point that takes one struct of arguments.
+
+    The struct is packed by a format of its members' types and passed as bytes: a call of a few microseconds has no
+    time for a ctypes structure, which takes two."""
+
+    def __init__(self, name, args):
+        letter = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i", ctypes.c_float: "f"}
+        self.name, self.fn = name, None
+        self.pack = struct.Struct("@" + "".join(letter[t] for _, t in args._fields_)).pack
+
+    def __call__(self, device, stream, *args):
+        """The call, on the tensors' device and its current stream."""
+        if self.fn is None:
+            self.fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)((self.name, _lib.lib()))
+        try:
+            a = self.pack(*args)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"{self.name}: an argument is no number of its type: {e}") from None
+        if torch._C._cuda_getDevice() == device:
+            rc = self.fn(a, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
+        else:
+            with torch.cuda.device(device):
+                rc = self.fn(a, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
+        if rc < 0:
+            check(rc)
+
+
+_linear = _Op("gdit_linear", _lib.gdit_linear_args)
+_norm_residual = _Op("gdit_norm_residual", _lib.gdit_norm_args)
+_attention = _Op("gdit_attention", _lib.gdit_attention_args)
 
 
 def _code(table, key, what):
@@ -48,8 +82,8 @@ def _rows(t, name, device, rows, cols):
     """Row stride of a [rows, cols] matrix with dense rows."""
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be dense")
@@ -61,29 +95,28 @@ def _rows(t, name, device, rows, cols):
 
 
 def _vector(t, name, device, shape, dtype=_f32):
+    """Address of an optional contiguous vector or table."""
     if t is None:
-        return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor on {device}")
+        return 0
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
 
 def _device(t, name):
-    d = t.device
-    if d.type != "cuda":
+    d = t.get_device()
+    if d < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
     return d
 
 
-def _run(fn, args, device, stream):
-    """The call, on the tensors' device and its current stream."""
-    if torch.cuda.current_device() == device.index:
-        check(fn(byref(args), torch.cuda.current_stream().cuda_stream if stream is None else stream))
-        return
-    with torch.cuda.device(device):
-        check(fn(byref(args), torch.cuda.current_stream().cuda_stream if stream is None else stream))
+def _matrix(like, rows, cols, dtype):
+    """A new [rows, cols] matrix on the device of `like`."""
+    if like.dtype is dtype and like.shape == (rows, cols) and like.is_contiguous():
+        return torch.empty_like(like)   # the quickest way to one
+    return like.new_empty((rows, cols), dtype=dtype)
 
 
 def linear(x, w, bias=None, *, activation="none", residual=None, out=None, out_dtype=None, stream=None):
@@ -103,28 +136,27 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out=None, out_d
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else _bf16
     code = _dtype(out_dtype, "out_dtype")
-    ldr, res = n, None
+    ldr, res = n, 0
     if residual is not None:
         if residual.dtype != out_dtype:
             raise TypeError(f"residual is {residual.dtype}, the output {out_dtype}: they must be the same")
         ldr, res = _rows(residual, "residual", d, m, n), residual.data_ptr()
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=d)
+        out = _matrix(x if residual is None else residual, m, n, out_dtype)
         ldo = n
     else:
         if out.dtype != out_dtype:
             raise TypeError(f"out is {out.dtype}, expected {out_dtype}")
         ldo = _rows(out, "out", d, m, n)
-    a = _lib.gdit_linear_args(x.data_ptr(), w.data_ptr(), _vector(bias, "bias", d, (n,)), res, out.data_ptr(), m, ldx,
-                              ldw, ldr, ldo, n, k, code, _code(ACTIVATIONS, activation, "activation"))
-    _run(_lib.gdit_linear, a, d, stream)
+    _linear(d, stream, x.data_ptr(), w.data_ptr(), _vector(bias, "bias", d, (n,)), res, out.data_ptr(), m, ldx, ldw, ldr,
+            ldo, n, k, code, _code(ACTIVATIONS, activation, "activation"))
     return out
 
 
 def _groups(t, name, device, dim):
     """(pointer, groups) of a [dim] or [groups, dim] table."""
     if t is None:
-        return None, 1
+        return 0, 1
     groups = 1 if t.dim() == 1 else t.shape[0]
     if groups < 1:
         raise ValueError(f"{name} has no group")
@@ -152,7 +184,7 @@ def norm_residual(h, y=None, *, post=None, post_gain=None, post_bias=None, gate=
     hd = _dtype(h.dtype, "h")
     pre_code, post_code = _code(NORMS, pre, "pre"), _code(NORMS, post, "post")
     ldh = _rows(h, "h", d, rows, dim)
-    ldy, yp, yd = dim, None, GDIT_BF16
+    ldy, yp, yd = dim, 0, GDIT_BF16
     if y is not None:
         ldy, yp, yd = _rows(y, "y", d, rows, dim), y.data_ptr(), _dtype(y.dtype, "y")
     elif post_code or post_gain is not None or post_bias is not None or gate is not None:
@@ -163,7 +195,7 @@ def norm_residual(h, y=None, *, post=None, post_gain=None, post_bias=None, gate=
     if scale is not None and shift is not None and g1 != g2:
         raise ValueError(f"scale has {g1} groups, shift {g2}")
     mod_groups = g1 if scale is not None else g2
-    rg = None
+    rg = 0
     if row_group is not None:
         rg = _vector(row_group, "row_group", d, (rows,), _i32)
     elif gate_groups > 1 or mod_groups > 1:
@@ -173,12 +205,12 @@ def norm_residual(h, y=None, *, post=None, post_gain=None, post_bias=None, gate=
     if not pre_code and (pre_gain is not None or pre_bias is not None):
         raise ValueError("pre_gain and pre_bias need pre")
     want_h = y is not None or residual_scale != 1.0 or out_h is not None
-    want_u = bool(pre_code) or scp is not None or shp is not None or out_u is not None or u_dtype is not None
+    want_u = bool(pre_code) or scale is not None or shift is not None or out_u is not None or u_dtype is not None
     ldoh = ldou = dim
-    ohp = oup = None
+    ohp = oup = 0
     if want_h:
         if out_h is None:
-            out_h = torch.empty((rows, dim), dtype=h.dtype, device=d)
+            out_h = _matrix(h, rows, dim, h.dtype)
         else:
             if out_h.dtype != h.dtype:
                 raise TypeError(f"out_h is {out_h.dtype}, h is {h.dtype}: they must be the same")
@@ -190,7 +222,7 @@ def norm_residual(h, y=None, *, post=None, post_gain=None, post_bias=None, gate=
             u_dtype = out_u.dtype if out_u is not None else y.dtype if y is not None else _bf16
         ud = _dtype(u_dtype, "u_dtype")
         if out_u is None:
-            out_u = torch.empty((rows, dim), dtype=u_dtype, device=d)
+            out_u = _matrix(h if y is None else y, rows, dim, u_dtype)
         else:
             if out_u.dtype != u_dtype:
                 raise TypeError(f"out_u is {out_u.dtype}, expected {u_dtype}")
@@ -198,17 +230,17 @@ def norm_residual(h, y=None, *, post=None, post_gain=None, post_bias=None, gate=
         oup = out_u.data_ptr()
     if not want_h and not want_u:
         raise ValueError("nothing to compute: give y, a residual_scale, pre, scale or shift")
-    a = _lib.gdit_norm_args(h.data_ptr(), yp, ohp, oup, _vector(post_gain, "post_gain", d, (dim,)),
-                            _vector(post_bias, "post_bias", d, (dim,)), gp, _vector(pre_gain, "pre_gain", d, (dim,)),
-                            _vector(pre_bias, "pre_bias", d, (dim,)), scp, shp, rg, rows, ldh, ldy, ldoh, ldou, dim,
-                            hd, yd, ud, post_code, pre_code, gate_groups, mod_groups, residual_scale, eps)
-    _run(_lib.gdit_norm_residual, a, d, stream)
+    vec = (dim,)
+    _norm_residual(d, stream, h.data_ptr(), yp, ohp, oup, _vector(post_gain, "post_gain", d, vec),
+                   _vector(post_bias, "post_bias", d, vec), gp, _vector(pre_gain, "pre_gain", d, vec),
+                   _vector(pre_bias, "pre_bias", d, vec), scp, shp, rg, rows, ldh, ldy, ldoh, ldou, dim, hd, yd, ud,
+                   post_code, pre_code, gate_groups, mod_groups, residual_scale, eps)
     return (out_h if want_h else h), (out_u if want_u else None)
 
 
 def _heads(t, name, device):
-    if t.dtype != _bf16 or t.device != device:
-        raise TypeError(f"{name} must be a bfloat16 tensor on {device}")
+    if t.dtype is not _bf16 or t.get_device() != device:
+        raise TypeError(f"{name} must be a bfloat16 tensor on cuda:{device}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
     n, heads, dim = t.shape
@@ -241,19 +273,20 @@ def attention(q, k, v, cu_q, cu_k, *, max_q, max_k, causal=True, scale=None, k_l
         raise ValueError("cu_q must be [batch + 1]")
     batch = cu_q.shape[0] - 1
     if out is None:
-        out = torch.empty((tq, heads, dim), dtype=_bf16, device=d)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((tq, heads, dim))
         ot, oh = heads * dim, dim
     else:
         to, ho, do, ot, oh = _heads(out, "out", d)
         if out.shape != q.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    lse = torch.empty((tq, heads), dtype=_f32, device=d) if return_lse else None
-    a = _lib.gdit_attention_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr() if return_lse else None, _vector(cu_q, "cu_q", d, (batch + 1,), _i32),
-                                 _vector(cu_k, "cu_k", d, (batch + 1,), _i32), _vector(k_len, "k_len", d, (batch,), _i32),
-                                 tq, tk, qt, qh, kt, kh, vt, vh, ot, oh, batch, heads, kv_heads, dim, max_q, max_k,
-                                 bool(causal), dim ** -0.5 if scale is None else scale)
-    _run(_lib.gdit_attention, a, d, stream)
+    lse, lp = None, 0
+    if return_lse:
+        lse = q.new_empty((tq, heads), dtype=_f32)
+        lp = lse.data_ptr()
+    _attention(d, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp,
+               _vector(cu_q, "cu_q", d, (batch + 1,), _i32), _vector(cu_k, "cu_k", d, (batch + 1,), _i32),
+               _vector(k_len, "k_len", d, (batch,), _i32), tq, tk, qt, qh, kt, kh, vt, vh, ot, oh, batch, heads, kv_heads,
+               dim, max_q, max_k, bool(causal), dim ** -0.5 if scale is None else scale)
     return (out, lse) if return_lse else out
 
 
