@@ -65,9 +65,10 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 // are turned into probabilities while the tensor core multiplies for the other.
 //
 //   rows kernel (KEYS = false)  the halves are neighbouring positions and go over the same keys: prompts
-//   keys kernel (KEYS = true)   the halves have the same rows and take turns at the blocks of 128 keys, and the CTAs of a
-//                               cluster take a part of the keys each: single tokens and too few tiles for the SMs.  The
-//                               partial outputs are joined in the order of the parts, through distributed shared memory.
+//   keys kernel (KEYS = true)   the halves have the same rows, 64 at most, and take turns at the blocks of 128 keys, and the
+//                               CTAs of a cluster take a part of the keys each: single tokens and too few tiles for the SMs.
+//                               Two warps of each half are left over: they join the partial outputs, in the order of the
+//                               parts, through distributed shared memory, while the others go on with the next tile.
 //
 //   warp 0       Q boxes, K and V tiles of 128 keys by TMA, each kind into a ring of its own
 //   warp 1       tcgen05.mma: S = Q K^T (f32, TMEM)
@@ -89,6 +90,7 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 
 constexpr int kAtBM = 128;       // rows of a half
 constexpr int kAtBN = 128;       // keys of a block
+constexpr int kAtKeyRows = 64;   // rows of a tile of the keys kernel, of the 128 that the tensor core computes
 constexpr int kAtThreads = 384;
 constexpr int kAtColS = 0, kAtColP = 128, kAtColO = 256;   // TMEM: S; P of the halves (64 columns each); O of the halves (128)
 // Registers of a thread: 168 at launch (64512 in all), then 104 for the first
@@ -100,9 +102,9 @@ template <int DP, bool KEYS>   // head_dim rounded up to 64 or 128
 struct AttnCfg {
   static constexpr int BOX = kAtBN * 128;                    // bytes of a [128][64] box
   static constexpr int TILE = BOX * (DP / 64);
-  static constexpr int Q = (KEYS ? 1 : 2) * TILE;
-  static constexpr int PART = KEYS ? kAtBM * DP * 4 : 0;     // f32 partial output of the CTA
-  static constexpr int STATS = KEYS ? kAtBM * 8 : 0;         // maximum and sum of its rows
+  static constexpr int Q = 2 * TILE / (KEYS ? 2 : 1);        // two halves, or two tiles' 64 rows
+  static constexpr int PART = KEYS ? 2 * kAtKeyRows * DP * 4 : 0;   // f32 partial outputs of the halves
+  static constexpr int STATS = KEYS ? 2 * kAtKeyRows * 8 : 0;       // maximum and sum of their rows
   static constexpr int BARS = 384;
   static constexpr int RING = 227 * 1024 - 128 - 1024 - Q - PART - STATS - BARS;   // 128: static shared memory
   static constexpr int SLOTS = RING / TILE < 10 ? RING / TILE : 10;
@@ -253,13 +255,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stats) + Cfg::STATS);
   uint64_t* empty = full + SLOTS;
   uint64_t* qfull = empty + SLOTS;
-  uint64_t* qempty = qfull + 1;
-  uint64_t* sfull = qempty + 1;              // [2]
+  uint64_t* qempty = qfull + 2;              // [2] each (the rows kernel has one Q buffer)
+  uint64_t* sfull = qempty + 2;              // [2]
   uint64_t* sfree = sfull + 2;               // the scores have been read
   uint64_t* pfull = sfree + 1;               // [2]
   uint64_t* ofull = pfull + 2;               // [2]: P V of a block is done
-  uint64_t* hfull = ofull + 2;               // half 1's part is in shared memory
-  uint64_t* jfull = hfull + 1;               // the parts of all CTAs are
+  uint64_t* jfull = ofull + 2;               // the parts of all CTAs are in their shared memory
   uint64_t* jempty = jfull + 1;              // and have been read by all
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -267,13 +268,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int worker = blockIdx.x / splits, workers = gridDim.x / splits;
   if (threadIdx.x == 0) {
     for (int i = 0; i < SLOTS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&sfull[s], 1), mbar_init(&pfull[s], 4), mbar_init(&ofull[s], 1);
-    mbar_init(sfree, 4);
-    mbar_init(hfull, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 1), mbar_init(&qempty[s], 1);
+      mbar_init(&sfull[s], 1), mbar_init(&pfull[s], KEYS ? 2 : 4), mbar_init(&ofull[s], 1);
+    }
+    mbar_init(sfree, KEYS ? 2 : 4);
     mbar_init(jfull, 4 * splits);
-    mbar_init(jempty, 8 * splits);
+    mbar_init(jempty, 4 * splits);
     fence_mbar_init();
     s_abort = 0;
     tma_prefetch_desc(&tmQ);
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   pdl_launch_dependents();
 
   const int group = a.heads / a.kv_heads;
-  const int half_pos = kAtBM / group;                 // positions of a half
+  const int half_pos = (KEYS ? kAtKeyRows : kAtBM) / group;   // positions of a half
   const int tile_pos = KEYS ? half_pos : 2 * half_pos;
   TileWalk walk;
   AttnTile t;
@@ -310,14 +311,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
            ok && walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
         if (t.nb == 0) continue;
         if (lane == 0) {
-          ok = op_wait(qempty, (nq & 1) ^ 1u, &s_abort);
+          const int qb = KEYS ? nq & 1 : 0;
+          ok = op_wait(&qempty[qb], ((KEYS ? nq >> 1 : nq) & 1) ^ 1u, &s_abort);
           if (ok) {
             const int halves = !KEYS && t.np > half_pos ? 2 : 1;
-            mbar_arrive_expect_tx(qfull, halves * boxes * half_pos * group * 128);
+            mbar_arrive_expect_tx(&qfull[qb], halves * boxes * half_pos * group * 128);
             for (int s = 0; s < halves; ++s)
               for (int x = 0; x < boxes; ++x)
-                tma_load_3d(sQ + s * Cfg::TILE + x * Cfg::BOX, &tmQ, qfull, x * 64, t.kvh * group,
-                            t.s.q0 + t.p0 + s * half_pos);
+                tma_load_3d(sQ + (KEYS ? qb * (Cfg::Q / 2) + x * (Cfg::BOX / 2) : s * Cfg::TILE + x * Cfg::BOX), &tmQ,
+                            &qfull[qb], x * 64, t.kvh * group, t.s.q0 + t.p0 + s * half_pos);
           }
           // the order of use: K of the first blocks, then V of a block and K of a later one in turn
           const int ahead = min(KEYS ? 3 : 2, t.nb), turns = 2 * (t.nb - ahead);
@@ -353,14 +355,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const uint32_t d = uniform(tmem) + kAtColS, bars = uniform(smem_u32(full));
       const uint32_t q0 = desc_lo_k(uniform(smem_u32(sQ))), k0 = desc_lo_k(uniform(smem_u32(sKV)));
       auto at = [&](const uint64_t* bar) { return bars + (uint32_t)((bar - full) * 8); };
-      uint32_t slot = 0, phase = 0, qphase = 0, sphase = 1;
+      uint32_t slot = 0, phase = 0, sphase = 1, nq = 0;
       for (long long round = 0;
            walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
         const int nb = (int)uniform(t.nb);
         const bool two = !KEYS && uniform(t.np > half_pos) != 0;   // both halves share each block
         if (nb == 0) continue;
-        op_wait_through(qfull, qphase, &s_abort);
-        qphase ^= 1u;
+        const uint32_t qb = KEYS ? nq & 1 : 0;
+        op_wait_through(&qfull[qb], (KEYS ? nq >> 1 : nq) & 1, &s_abort);
+        ++nq;
         for (int j = 0; j < nb; ++j) {
           op_wait_through(&full[slot], phase, &s_abort);
           const uint32_t k = k0 + slot * (Cfg::TILE >> 4);
@@ -368,10 +371,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             op_wait_through(sfree, sphase, &s_abort);
             sphase ^= 1u;
             tc_fence_after();
-            const uint32_t q = q0 + (KEYS ? 0 : s * (Cfg::TILE >> 4));
+            // (the keys kernel's Q tile has 64 rows; what is read behind them belongs to rows that nobody looks at)
+            const uint32_t q = q0 + (KEYS ? qb * (Cfg::Q / 2 >> 4) : s * (Cfg::TILE >> 4));
             auto step = [&](int x) {
-              const uint32_t o = ((x >> 2) * Cfg::BOX + (x & 3) * 32) >> 4;
-              umma_bf16_lo(d, q + o, k + o, idesc, x > 0);
+              const uint32_t o = (x & 3) * 32, b = (x >> 2) * Cfg::BOX;
+              umma_bf16_lo(d, q + ((KEYS ? b / 2 : b) + o >> 4), k + (b + o >> 4), idesc, x > 0);
             };
             if (elect_one()) {
               if (ksteps == DP / 16) {
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               umma_commit_at(at(sfull) + s * 8);
               if (closes) {
                 umma_commit_at(at(empty) + slot * 8);
-                if (j == nb - 1) umma_commit_at(at(qempty));   // Q has been used for the last time
+                if (j == nb - 1) umma_commit_at(at(qempty) + qb * 8);   // Q has been used for the last time
               }
             }
           };
@@ -466,7 +470,61 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const float c = fabsf(a.scale_log2);
     const uint64_t c2 = f2_splat(c);
     uint32_t sphase = 0, ophase = 0, tphase = 0;
-    for (long long round = 0;
+    if (KEYS && (warp & 2)) {
+      // join: the parts (two of each CTA) of some rows, added up in their order
+      const int w = s * 2 + (warp & 1), parts = 2 * splits;
+      for (long long round = 0;
+           walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
+        ok = op_wait_warp_cluster(jfull, tphase, &s_abort);
+        if (!ok) break;
+        tphase ^= 1u;
+        const int rows = t.np * group;
+        for (int i = rank + splits * w; i < rows; i += splits * 4) {
+          float2 st = make_float2(-INFINITY, 0.f);   // lane: of part `lane`
+          if (lane < parts) st = ld_cluster_f2(mapa_shared(stats + (lane & 1) * kAtKeyRows + i, lane >> 1));
+          float m = st.x;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+          m = __shfl_sync(~0u, m, 0);
+          const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
+          float l = st.y * f;
+          if (f == 0.f) l = 0.f;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+          l = __shfl_sync(~0u, l, 0);
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          const uint32_t at = (uint32_t)(i * DP * 4 + ((lane ^ (i & 7)) << 4));
+          for (int p0 = 0; p0 < parts; p0 += 2) {
+            float4 h[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              if (lane * 4 < DP) h[p] = ld_cluster_f4(mapa_shared(part + p * kAtKeyRows * DP, p0 >> 1) + at);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const float fp = __shfl_sync(~0u, f, p0 + p);
+              if (fp != 0.f && lane * 4 < DP)   // a part without keys holds nothing
+                o.x = fmaf(h[p].x, fp, o.x), o.y = fmaf(h[p].y, fp, o.y), o.z = fmaf(h[p].z, fp, o.z), o.w = fmaf(h[p].w, fp, o.w);
+            }
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int ip = i / group, head = t.kvh * group + i - ip * group;
+          const long long token = t.s.q0 + t.p0 + ip;
+          __nv_bfloat16* dst = a.out + token * a.o_t + head * a.o_h + lane * 4;
+          if (lane * 4 < a.dim) {
+            if (out_mode > 0) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            } else {
+              dst[0] = __float2bfloat16_rn(o.x * inv), dst[1] = __float2bfloat16_rn(o.y * inv);
+              dst[2] = __float2bfloat16_rn(o.z * inv), dst[3] = __float2bfloat16_rn(o.w * inv);
+            }
+          }
+          if (lane == 0 && a.lse != nullptr)
+            a.lse[token * a.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+        }
+        __syncwarp();
+        if (lane < splits) mbar_arrive_cluster(mapa_shared(jempty, lane));
+      }
+    } else for (long long round = 0;
          walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
       const int first_pos = KEYS ? 0 : s * half_pos;   // of this half in the tile
       if (first_pos >= t.np) continue;
@@ -583,96 +641,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.69314718055994531f;
         tc_fence_before();   // these reads of O come before what the next tile's first block lets the tensor core write
       } else {
-        // join: half 1 puts its output into `part`, half 0 adds its own, then every CTA adds up all parts of some of the rows
+        // this part of the rows for the join, after all CTAs have read the previous tile's
         ok = op_wait_warp_cluster(jempty, tphase ^ 1u, &s_abort);
-        if (ok && s == 0) ok = op_wait_warp(hfull, tphase, &s_abort);
         if (!ok) break;
+        tphase ^= 1u;
         if (active) {
-          float own = 1.f, other = 0.f;
-          if (s == 0) {
-            const float2 st = stats[row];
-            const float m = fmaxf(top, st.x);
-            own = top == -INFINITY ? 0.f : ex2((top - m) * c);
-            other = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
-            top = m;
-            sum = sum * own + st.y * other;
-          }
+          float* dst = part + (s * kAtKeyRows + row) * DP;
+          if (done > 0) {
 #pragma unroll 1
-          for (int x = 0; x < a.dim; x += 32) {
-            float v[32] = {};
-            if (done > 0) {
+            for (int x = 0; x < a.dim; x += 32) {
+              float v[32];
               tmem_ld32(tO + x, reinterpret_cast<uint32_t(&)[32]>(v));
               tmem_ld_wait();
-            }
 #pragma unroll
-            for (int y = 0; y < 32; y += 4) {   // 16-byte pieces of a row in an order of its own: no bank conflicts
-              float4* p = reinterpret_cast<float4*>(part + row * DP) + (((x + y) >> 2) ^ (row & 7));
-              float4 o = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
-              if (s == 0) {
-                const float4 h = *p;
-                // a half without keys counts nothing, whatever it holds
-                o.x = own == 0.f ? 0.f : o.x * own, o.y = own == 0.f ? 0.f : o.y * own;
-                o.z = own == 0.f ? 0.f : o.z * own, o.w = own == 0.f ? 0.f : o.w * own;
-                if (other != 0.f)
-                  o.x = fmaf(h.x, other, o.x), o.y = fmaf(h.y, other, o.y), o.z = fmaf(h.z, other, o.z),
-                  o.w = fmaf(h.w, other, o.w);
-              }
-              *p = o;
+              for (int y = 0; y < 32; y += 4)   // 16-byte pieces of a row in an order of its own: no bank conflicts
+                reinterpret_cast<float4*>(dst)[((x + y) >> 2) ^ (row & 7)] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
             }
           }
-          stats[row] = make_float2(top, sum);
+          stats[s * kAtKeyRows + row] = make_float2(top, sum);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (s == 1) mbar_arrive(hfull);
-          else
-            for (int r = 0; r < splits; ++r) mbar_arrive_cluster(mapa_shared(jfull, r));
-        }
-        ok = op_wait_warp_cluster(jfull, tphase, &s_abort);
-        if (!ok) break;
-        const int rows = t.np * group;
-        for (int i = rank + splits * (warp - 4); i < rows; i += splits * 8) {
-          float2 st[8];
-          float m = -INFINITY, l = 0.f;
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            if (r < splits) st[r] = ld_cluster_f2(mapa_shared(stats + i, r));
-            else st[r] = make_float2(-INFINITY, 0.f);
-            m = fmaxf(m, st[r].x);
-          }
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          const uint32_t at = (uint32_t)(i * DP * 4 + ((lane ^ (i & 7)) << 4));
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            if (st[r].x == -INFINITY) continue;
-            const float f = ex2((st[r].x - m) * c);
-            l = fmaf(st[r].y, f, l);
-            if (lane * 4 < DP) {
-              const float4 h = ld_cluster_f4(mapa_shared(part, r) + at);
-              o.x = fmaf(h.x, f, o.x), o.y = fmaf(h.y, f, o.y), o.z = fmaf(h.z, f, o.z), o.w = fmaf(h.w, f, o.w);
-            }
-          }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const int ip = i / group, head = t.kvh * group + i - ip * group;
-          const long long token = t.s.q0 + t.p0 + ip;
-          __nv_bfloat16* dst = a.out + token * a.o_t + head * a.o_h + lane * 4;
-          if (lane * 4 < a.dim) {
-            if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (out_mode > 0) {
-              *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            } else {
-              dst[0] = __float2bfloat16_rn(o.x * inv), dst[1] = __float2bfloat16_rn(o.y * inv);
-              dst[2] = __float2bfloat16_rn(o.z * inv), dst[3] = __float2bfloat16_rn(o.w * inv);
-            }
-          }
-          if (lane == 0 && a.lse != nullptr)
-            a.lse[token * a.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
-        }
-        __syncwarp();
-        if (lane == 0)
-          for (int r = 0; r < splits; ++r) mbar_arrive_cluster(mapa_shared(jempty, r));
-        tphase ^= 1u;
+        if (lane < splits) mbar_arrive_cluster(mapa_shared(jfull, lane));
       }
     }
   }
@@ -713,12 +703,14 @@ void launch_attention_as(const AttnArgs& a, const CUtensorMap& mq, const CUtenso
 }
 
 inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
-  const int group = a.heads / a.kv_heads, half_pos = kAtBM / group;
+  const int group = a.heads / a.kv_heads;
   // tiles of `pos` positions that the sequences can have at most
   auto tiles = [&](int pos) { return std::min(a.total_q, a.total_q / pos + a.batch); };
-  // Rows that fill no second half, or too few tiles for the SMs: the halves,
-  // and the CTAs of a cluster, take parts of the keys instead.
-  const bool keys = a.max_q <= half_pos || tiles(2 * half_pos) * a.kv_heads * 2 <= sms;
+  // Positions of a 64-row tile are all there are, or too few 256-row tiles for the
+  // SMs: the halves, and the CTAs of a cluster, take parts of the keys instead.
+  const bool keys = group <= kAtKeyRows &&
+                    (a.max_q <= kAtKeyRows / group || tiles(2 * (kAtBM / group)) * a.kv_heads * 2 <= sms);
+  const int half_pos = (keys ? kAtKeyRows : kAtBM) / group;
   a.max_tiles = tiles(keys ? half_pos : 2 * half_pos);
   int splits = 1;
   if (keys) {

@@ -74,12 +74,33 @@ __device__ __forceinline__ void op_wait_through(uint64_t* bar, uint32_t parity, 
   if (__builtin_expect(!mbar_try_wait(bar, parity), 0)) op_wait(bar, parity, abort);
 }
 
-// The same for a barrier that other CTAs of the cluster arrive at: what they
+// op_wait_warp for a barrier that other CTAs of the cluster arrive at: what they
 // wrote to shared memory before is visible then.
 __device__ __forceinline__ bool op_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = op_wait_warp(bar, parity, abort);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return ok;
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) {
+    auto ready = [&] {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(r)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSleepNs)
+          : "memory");
+      return r != 0;
+    };
+    const unsigned long long t0 = globaltimer_ns();
+    while (!(ok = ready())) {
+      if (*abort) break;
+      if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+        *abort = 1;
+        atomicOr(&g_op_status, DEV_ERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  return __shfl_sync(~0u, ok, 0) != 0;
 }
 
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
