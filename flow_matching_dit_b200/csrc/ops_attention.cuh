@@ -1,6 +1,8 @@
 // gdit_attention: softmax attention over packed sequences with grouped heads.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_tc.cuh"
 #include "ops_common.cuh"
 
@@ -64,8 +66,8 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 // warpgroup, scores and an output of its own in TMEM, so that one half's scores
 // are turned into probabilities while the tensor core multiplies for the other.
 //
-//   rows kernel (KEYS = false)  the halves are neighbouring positions and go over the same keys: prompts
-//   keys kernel (KEYS = true)   the halves have the same rows, 64 at most, and take turns at the blocks of 128 keys, and the
+//   rows kernel (ROWS = 0)      the halves are neighbouring positions and go over the same keys: prompts
+//   keys kernel (ROWS = 64, 16) the halves have the same rows, so many at most, and take turns at the blocks of 128 keys, and the
 //                               CTAs of a cluster take a part of the keys each: single tokens and too few tiles for the SMs.
 //                               Two warps of each half are left over: they join the partial outputs, in the order of the
 //                               parts, through distributed shared memory, while the others go on with the next tile.
@@ -90,7 +92,6 @@ __device__ __forceinline__ void report_bad_seqs(const AttnArgs& a, int tid, int 
 
 constexpr int kAtBM = 128;       // rows of a half
 constexpr int kAtBN = 128;       // keys of a block
-constexpr int kAtKeyRows = 64;   // rows of a tile of the keys kernel, of the 128 that the tensor core computes
 constexpr int kAtThreads = 384;
 constexpr int kAtColS = 0, kAtColP = 128, kAtColO = 256;   // TMEM: S; P of the halves (64 columns each); O of the halves (128)
 // Registers of a thread: 168 at launch (64512 in all), then 104 for the first
@@ -98,17 +99,22 @@ constexpr int kAtColS = 0, kAtColP = 128, kAtColO = 256;   // TMEM: S; P of the 
 constexpr int kAtRegs = 168, kAtRegsIssue = 104, kAtRegsSoftmax = 200;
 static_assert(3 * kAtRegs == kAtRegsIssue + 2 * kAtRegsSoftmax, "register split");
 
-template <int DP, bool KEYS>   // head_dim rounded up to 64 or 128
+// DP: head_dim rounded up to 64 or 128.  ROWS: rows of a tile of the keys kernel
+// (64, or 16), of the 128 that the tensor core computes; 0 is the rows kernel.
+template <int DP, int ROWS>
 struct AttnCfg {
+  static constexpr bool KEYS = ROWS > 0;
   static constexpr int BOX = kAtBN * 128;                    // bytes of a [128][64] box
   static constexpr int TILE = BOX * (DP / 64);
-  static constexpr int Q = 2 * TILE / (KEYS ? 2 : 1);        // two halves, or two tiles' 64 rows
-  static constexpr int PART = KEYS ? 2 * kAtKeyRows * DP * 4 : 0;   // f32 partial outputs of the halves
-  static constexpr int STATS = KEYS ? 2 * kAtKeyRows * 8 : 0;       // maximum and sum of their rows
+  static constexpr int QBOX = KEYS ? ROWS * 128 : BOX;       // of a [rows][64] box of Q
+  static constexpr int Q = 2 * QBOX * (DP / 64);             // two halves, or two tiles
+  static constexpr int PART = KEYS ? 2 * ROWS * DP * 4 : 0;   // f32 partial outputs of the halves
+  static constexpr int STATS = KEYS ? 2 * ROWS * 8 : 0;       // maximum and sum of their rows
   static constexpr int BARS = 384;
   static constexpr int RING = 227 * 1024 - 128 - 1024 - Q - PART - STATS - BARS;   // 128: static shared memory
   static constexpr int SLOTS = RING / TILE < 10 ? RING / TILE : 10;
   static constexpr int SMEM = 1024 + Q + PART + STATS + BARS + SLOTS * TILE;
+  static constexpr int WARPS = KEYS ? (ROWS + 31) / 32 : 4;   // of a half that have rows
   static_assert((2 * SLOTS + 16) * 8 <= BARS, "barriers");
 };
 
@@ -238,11 +244,12 @@ __device__ __forceinline__ void store_out_row(__nv_bfloat16* o, int mode, int c0
   }
 }
 
-template <int DP, bool KEYS>
+template <int DP, int ROWS>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const AttnArgs a, int splits, int out_mode) {
-  using Cfg = AttnCfg<DP, KEYS>;
+  using Cfg = AttnCfg<DP, ROWS>;
+  constexpr bool KEYS = ROWS > 0;
   constexpr int SLOTS = Cfg::SLOTS, KS = (SLOTS + 1) / 2, VS = SLOTS / 2;   // ring of K tiles, ring of V tiles behind it
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_holder;
@@ -270,10 +277,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     for (int i = 0; i < SLOTS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&qfull[s], 1), mbar_init(&qempty[s], 1);
-      mbar_init(&sfull[s], 1), mbar_init(&pfull[s], KEYS ? 2 : 4), mbar_init(&ofull[s], 1);
+      mbar_init(&sfull[s], 1), mbar_init(&pfull[s], Cfg::WARPS), mbar_init(&ofull[s], 1);
     }
-    mbar_init(sfree, KEYS ? 2 : 4);
-    mbar_init(jfull, 4 * splits);
+    mbar_init(sfree, Cfg::WARPS);
+    mbar_init(jfull, 2 * Cfg::WARPS * splits);
     mbar_init(jempty, 4 * splits);
     fence_mbar_init();
     s_abort = 0;
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   pdl_launch_dependents();
 
   const int group = a.heads / a.kv_heads;
-  const int half_pos = (KEYS ? kAtKeyRows : kAtBM) / group;   // positions of a half
+  const int half_pos = (KEYS ? ROWS : kAtBM) / group;   // positions of a half
   const int tile_pos = KEYS ? half_pos : 2 * half_pos;
   TileWalk walk;
   AttnTile t;
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_arrive_expect_tx(&qfull[qb], halves * boxes * half_pos * group * 128);
             for (int s = 0; s < halves; ++s)
               for (int x = 0; x < boxes; ++x)
-                tma_load_3d(sQ + (KEYS ? qb * (Cfg::Q / 2) + x * (Cfg::BOX / 2) : s * Cfg::TILE + x * Cfg::BOX), &tmQ,
+                tma_load_3d(sQ + (KEYS ? qb : s) * (Cfg::Q / 2) + x * Cfg::QBOX, &tmQ,
                             &qfull[qb], x * 64, t.kvh * group, t.s.q0 + t.p0 + s * half_pos);
           }
           // the order of use: K of the first blocks, then V of a block and K of a later one in turn
@@ -371,11 +378,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             op_wait_through(sfree, sphase, &s_abort);
             sphase ^= 1u;
             tc_fence_after();
-            // (the keys kernel's Q tile has 64 rows; what is read behind them belongs to rows that nobody looks at)
-            const uint32_t q = q0 + (KEYS ? qb * (Cfg::Q / 2 >> 4) : s * (Cfg::TILE >> 4));
+            // (the keys kernel's Q tile has fewer rows; what is read behind them belongs to rows that nobody looks at)
+            const uint32_t q = q0 + (KEYS ? qb : s) * (Cfg::Q / 2 >> 4);
             auto step = [&](int x) {
-              const uint32_t o = (x & 3) * 32, b = (x >> 2) * Cfg::BOX;
-              umma_bf16_lo(d, q + ((KEYS ? b / 2 : b) + o >> 4), k + (b + o >> 4), idesc, x > 0);
+              const uint32_t o = (x & 3) * 32 >> 4, b = x >> 2;
+              umma_bf16_lo(d, q + b * (Cfg::QBOX >> 4) + o, k + b * (Cfg::BOX >> 4) + o, idesc, x > 0);
             };
             if (elect_one()) {
               if (ksteps == DP / 16) {
@@ -470,6 +477,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const float c = fabsf(a.scale_log2);
     const uint64_t c2 = f2_splat(c);
     uint32_t sphase = 0, ophase = 0, tphase = 0;
+    auto rescale = [&](float f) {   // row `row` of O times f
+#pragma unroll 1
+      for (int x = 0; x < a.dim; x += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + x, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+        tmem_st32(tO + x, o);
+      }
+    };
     if (KEYS && (warp & 2)) {
       // join: the parts (two of each CTA) of some rows, added up in their order
       const int w = s * 2 + (warp & 1), parts = 2 * splits;
@@ -481,7 +499,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int rows = t.np * group;
         for (int i = rank + splits * w; i < rows; i += splits * 4) {
           float2 st = make_float2(-INFINITY, 0.f);   // lane: of part `lane`
-          if (lane < parts) st = ld_cluster_f2(mapa_shared(stats + (lane & 1) * kAtKeyRows + i, lane >> 1));
+          if (lane < parts) st = ld_cluster_f2(mapa_shared(stats + (lane & 1) * ROWS + i, lane >> 1));
           float m = st.x;
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
@@ -498,7 +516,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             float4 h[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-              if (lane * 4 < DP) h[p] = ld_cluster_f4(mapa_shared(part + p * kAtKeyRows * DP, p0 >> 1) + at);
+              if (lane * 4 < DP) h[p] = ld_cluster_f4(mapa_shared(part + p * ROWS * DP, p0 >> 1) + at);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const float fp = __shfl_sync(~0u, f, p0 + p);
@@ -524,7 +542,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         __syncwarp();
         if (lane < splits) mbar_arrive_cluster(mapa_shared(jempty, lane));
       }
-    } else for (long long round = 0;
+    } else if ((warp & 3) < Cfg::WARPS) for (long long round = 0;
          walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
       const int first_pos = KEYS ? 0 : s * half_pos;   // of this half in the tile
       if (first_pos >= t.np) continue;
@@ -535,6 +553,71 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (a.causal && valid) limit = max(0, min(limit, pos + t.s.nk - t.s.nq + 1));
       float top = -INFINITY, sum = 0.f;
       int done = 0;                                    // blocks of this half
+      // ROWS = 16: a quad of lanes has the rows quad and quad + 8, two neighbouring keys of every eight a lane; in the
+      // layout of a thread a row the four rows of a token would cost the exponentials of 32.
+      float top2[2] = {-INFINITY, -INFINITY}, sum2[2] = {0.f, 0.f};
+      const bool upper = t.np * group > 8;             // rows 8 and up are there
+      auto few_rows = [&](int block, int done, auto& wait_o) {
+        tc_fence_after();
+        float v[64];
+        tmem_ld16x256(tS, reinterpret_cast<uint32_t(&)[64]>(v));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfree);
+        const int lim0 = __shfl_sync(~0u, limit, lane >> 2), lim1 = __shfl_sync(~0u, limit, (lane >> 2) + 8);
+        const int left0 = lim0 - block * kAtBN - 2 * (lane & 3), left1 = lim1 - block * kAtBN - 2 * (lane & 3);
+        if (!__all_sync(~0u, min(left0, left1) >= kAtBN)) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            v[x] = (x >> 2) * 8 + (x & 1) < ((x & 2) ? left1 : left0) ? v[x] : -INFINITY;
+        }
+        float m[2] = {top2[0], top2[1]};
+#pragma unroll
+        for (int x = 0; x < 64; x += 4) m[0] = max3(m[0], v[x], v[x + 1]), m[1] = max3(m[1], v[x + 2], v[x + 3]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          m[r] = fmaxf(m[r], __shfl_xor_sync(~0u, m[r], 1));
+          m[r] = fmaxf(m[r], __shfl_xor_sync(~0u, m[r], 2));
+        }
+        if (!wait_o()) return false;
+        tc_fence_after();
+        if (__any_sync(~0u, (m[0] - top2[0]) * c > 8.f || (m[1] - top2[1]) * c > 8.f)) {
+          float f[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            f[r] = top2[r] == -INFINITY ? 0.f : ex2((top2[r] - m[r]) * c);
+            sum2[r] *= f[r];
+            top2[r] = m[r];
+          }
+          const float g0 = __shfl_sync(~0u, f[0], (lane & 7) * 4), g1 = __shfl_sync(~0u, f[1], (lane & 7) * 4);
+          if (done > 0) rescale(lane < 8 ? g0 : g1);
+        }
+        uint32_t p[32];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float base = top2[r] == -INFINITY ? 0.f : -top2[r] * c;
+          float part_sum = 0.f;
+          if (r == 0 || upper) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float e0 = ex2(fmaf(v[4 * x + 2 * r], c, base)), e1 = ex2(fmaf(v[4 * x + 2 * r + 1], c, base));
+              part_sum += e0 + e1;
+              p[2 * x + r] = pack_bf16x2(e0, e1);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) p[2 * x + r] = 0;
+          }
+          sum2[r] += part_sum;
+        }
+        tmem_st16x128(tP, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[s]);
+        return true;
+      };
       for (int j = KEYS ? s : 0; j < t.nb; j += KEYS ? 2 : 1, ++done) {
         ok = op_wait_warp(&sfull[s], sphase, &s_abort);
         if (!ok) break;
@@ -547,6 +630,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           return ok;
         };
+        if constexpr (ROWS == 16) {
+          if (!few_rows(t.b0 + j, done, wait_o)) break;
+          continue;
+        }
         if (!active) {
           if (!wait_o()) break;
           if (lane == 0) mbar_arrive(sfree), mbar_arrive(&pfull[s]);
@@ -575,17 +662,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         // (an infinite difference included: the first block, or a row that saw nothing so far)
         if (__any_sync(~0u, (m - top) * c > 8.f)) {
           const float f = top == -INFINITY ? 0.f : ex2((top - m) * c);
-          if (done > 0) {
-#pragma unroll 1
-            for (int x = 0; x < a.dim; x += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + x, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st32(tO + x, o);
-            }
-          }
+          if (done > 0) rescale(f);
           sum *= f;
           top = m;
         }
@@ -641,12 +718,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.69314718055994531f;
         tc_fence_before();   // these reads of O come before what the next tile's first block lets the tensor core write
       } else {
+        if constexpr (ROWS == 16) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            sum2[r] += __shfl_xor_sync(~0u, sum2[r], 1);
+            sum2[r] += __shfl_xor_sync(~0u, sum2[r], 2);
+          }
+          const float t0 = __shfl_sync(~0u, top2[0], (lane & 7) * 4), t1 = __shfl_sync(~0u, top2[1], (lane & 7) * 4);
+          const float s0 = __shfl_sync(~0u, sum2[0], (lane & 7) * 4), s1 = __shfl_sync(~0u, sum2[1], (lane & 7) * 4);
+          top = lane < 8 ? t0 : t1, sum = lane < 8 ? s0 : s1;
+        }
         // this part of the rows for the join, after all CTAs have read the previous tile's
         ok = op_wait_warp_cluster(jempty, tphase ^ 1u, &s_abort);
         if (!ok) break;
         tphase ^= 1u;
         if (active) {
-          float* dst = part + (s * kAtKeyRows + row) * DP;
+          float* dst = part + (s * ROWS + row) * DP;
           if (done > 0) {
 #pragma unroll 1
             for (int x = 0; x < a.dim; x += 32) {
@@ -655,10 +742,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int y = 0; y < 32; y += 4)   // 16-byte pieces of a row in an order of its own: no bank conflicts
-                reinterpret_cast<float4*>(dst)[((x + y) >> 2) ^ (row & 7)] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                if (row < ROWS) reinterpret_cast<float4*>(dst)[((x + y) >> 2) ^ (row & 7)] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
             }
           }
-          stats[s * kAtKeyRows + row] = make_float2(top, sum);
+          if (row < ROWS) stats[s * ROWS + row] = make_float2(top, sum);
         }
         tc_fence_before();
         __syncwarp();
@@ -690,11 +777,11 @@ inline CUtensorMap make_heads_tmap(const __nv_bfloat16* p, long long tokens, int
   return m;
 }
 
-template <int DP, bool KEYS>
+template <int DP, int ROWS>
 void launch_attention_as(const AttnArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                          int splits, int sms, int out_mode, cudaStream_t s) {
-  using Cfg = AttnCfg<DP, KEYS>;
-  auto kern = attention_kernel<DP, KEYS>;
+  using Cfg = AttnCfg<DP, ROWS>;
+  auto kern = attention_kernel<DP, ROWS>;
   allow_smem(kern, Cfg::SMEM, kAtRegs);
   const int most = splits > 1 ? max_clusters(kern, splits, kAtThreads, Cfg::SMEM) : sms;
   const int workers = (int)std::min<long long>(a.max_tiles * a.kv_heads, most);
@@ -708,9 +795,9 @@ inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
   auto tiles = [&](int pos) { return std::min(a.total_q, a.total_q / pos + a.batch); };
   // Positions of a 64-row tile are all there are, or too few 256-row tiles for the
   // SMs: the halves, and the CTAs of a cluster, take parts of the keys instead.
-  const bool keys = group <= kAtKeyRows &&
-                    (a.max_q <= kAtKeyRows / group || tiles(2 * (kAtBM / group)) * a.kv_heads * 2 <= sms);
-  const int half_pos = (keys ? kAtKeyRows : kAtBM) / group;
+  const bool keys = group <= 64 && (a.max_q <= 64 / group || tiles(2 * (kAtBM / group)) * a.kv_heads * 2 <= sms);
+  const int rows = !keys ? 0 : group <= 16 && a.max_q <= 16 / group ? 16 : 64;
+  const int half_pos = (keys ? rows : kAtBM) / group;
   a.max_tiles = tiles(keys ? half_pos : 2 * half_pos);
   int splits = 1;
   if (keys) {
@@ -725,13 +812,14 @@ inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
     return (uintptr_t)a.out % bytes == 0 && a.o_t * 2 % bytes == 0 && a.o_h * 2 % bytes == 0;
   };
   const int out_mode = rows_aligned(32) ? 2 : rows_aligned(16) ? 1 : 0;
-  if (a.dim > 64) {
-    if (keys) launch_attention_as<128, true>(a, mq, mk, mv, splits, sms, out_mode, s);
-    else launch_attention_as<128, false>(a, mq, mk, mv, splits, sms, out_mode, s);
-  } else {
-    if (keys) launch_attention_as<64, true>(a, mq, mk, mv, splits, sms, out_mode, s);
-    else launch_attention_as<64, false>(a, mq, mk, mv, splits, sms, out_mode, s);
-  }
+  auto launch = [&](auto d) {
+    constexpr int DP = decltype(d)::value;
+    if (rows == 16) launch_attention_as<DP, 16>(a, mq, mk, mv, splits, sms, out_mode, s);
+    else if (rows == 64) launch_attention_as<DP, 64>(a, mq, mk, mv, splits, sms, out_mode, s);
+    else launch_attention_as<DP, 0>(a, mq, mk, mv, splits, sms, out_mode, s);
+  };
+  if (a.dim > 64) launch(std::integral_constant<int, 128>());
+  else launch(std::integral_constant<int, 64>());
 }
 
 }  // namespace gdit
