@@ -111,7 +111,7 @@ struct AttnCfg {
   static constexpr int PART = KEYS ? 2 * ROWS * DP * 4 : 0;   // f32 partial outputs of the halves
   static constexpr int STATS = KEYS ? 2 * ROWS * 8 : 0;       // maximum and sum of their rows
   static constexpr int BARS = 384;
-  static constexpr int RING = 227 * 1024 - 128 - 1024 - Q - PART - STATS - BARS;   // 128: static shared memory
+  static constexpr int RING = 227 * 1024 - (KEYS ? 384 : 128) - 1024 - Q - PART - STATS - BARS;   // 384, 128: static shared memory
   static constexpr int SLOTS = RING / TILE < 10 ? RING / TILE : 10;
   static constexpr int SMEM = 1024 + Q + PART + STATS + BARS + SLOTS * TILE;
   static constexpr int WARPS = KEYS ? (ROWS + 31) / 32 : 4;   // of a half that have rows
@@ -127,8 +127,7 @@ struct AttnTile {
 
 // Walks tiles in an order that all warps and CTAs agree on: all lanes of a warp
 // together.  A group of 32 sequences at a time, one a lane; within a group by
-// falling position (the longest tiles of causal prompts first), and in the keys
-// kernel by falling number of keys.
+// falling position (the longest tiles of causal prompts first).
 struct TileWalk {
   int base;              // first sequence of the group
   long long before;      // tiles in front of the group
@@ -136,40 +135,26 @@ struct TileWalk {
   int above;
   int mine;              // lane: tiles of its sequence
   Seq seq;
+  const uint8_t* order;  // the sequences by falling number of keys, or NULL
 
-  template <bool KEYS>
   __device__ __forceinline__ void load(const AttnArgs& a, int tile_pos) {
     const int lane = threadIdx.x & 31;
     seq = {0, 0, 0, 0};
     if (base + lane < a.batch) {
       bool ok;
-      const Seq s = read_seq(a, base + lane, ok);
+      const Seq s = read_seq(a, order != nullptr ? order[base + lane] : base + lane, ok);
       if (ok) seq = s;
-    }
-    if (KEYS) {   // most keys first, so that the last tiles to be handed out are short
-      int rank = 0, src = 0;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int nk = __shfl_sync(~0u, seq.nk, i);
-        rank += nk > seq.nk || (nk == seq.nk && i < lane);
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) src = __shfl_sync(~0u, rank, i) == lane ? i : src;
-      seq.q0 = __shfl_sync(~0u, seq.q0, src);
-      seq.nq = __shfl_sync(~0u, seq.nq, src);
-      seq.k0 = __shfl_sync(~0u, seq.k0, src);
-      seq.nk = __shfl_sync(~0u, seq.nk, src);
     }
     mine = seq.nq / tile_pos + (seq.nq % tile_pos != 0);
     level = __reduce_max_sync(~0u, mine);
     full = above = 0;
   }
 
-  template <bool KEYS>
-  __device__ __forceinline__ void start(const AttnArgs& a, int tile_pos) {
+  __device__ __forceinline__ void start(const AttnArgs& a, int tile_pos, const uint8_t* sorted) {
     base = 0;
     before = 0;
-    load<KEYS>(a, tile_pos);
+    order = sorted;
+    load(a, tile_pos);
   }
 
   // id = tile * kv_heads + key head, growing from call to call; false behind the last tile
@@ -184,7 +169,7 @@ struct TileWalk {
         before += full;
         base += 32;
         if (base >= a.batch) return false;
-        load<KEYS>(a, tile_pos);
+        load(a, tile_pos);
         continue;
       }
       --level;
@@ -208,6 +193,14 @@ struct TileWalk {
     return true;
   }
 };
+
+// The keys kernel, whose sequences mostly have one tile a key head, takes up to
+// kAtSorted sequences by falling number of keys, so that the last tiles to be handed
+// out are short.
+constexpr int kAtSorted = 256;
+// What a tile of the keys kernel costs beside its blocks (its first scores, its
+// last output, the join), in blocks.
+constexpr int kAtJoinBlocks = 2;
 
 // Position r of a walk over `count` workers in rounds that run back and forth:
 // with tiles of falling length everybody gets as much.
@@ -303,6 +296,24 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int group = a.heads / a.kv_heads;
   const int half_pos = (KEYS ? ROWS : kAtBM) / group;   // positions of a half
   const int tile_pos = KEYS ? half_pos : 2 * half_pos;
+  const uint8_t* sorted = nullptr;
+  if constexpr (KEYS) {
+    __shared__ uint8_t s_order[kAtSorted];
+    if (a.batch <= kAtSorted) {
+      int* keys = reinterpret_cast<int*>(part);   // free until the first tile is joined
+      bool fine;
+      int mine = 0;
+      if (threadIdx.x < a.batch) keys[threadIdx.x] = mine = read_seq(a, threadIdx.x, fine).nk;
+      __syncthreads();
+      if (threadIdx.x < a.batch) {
+        int before = 0;
+        for (int i = 0; i < a.batch; ++i) before += keys[i] > mine || (keys[i] == mine && i < (int)threadIdx.x);
+        s_order[before] = (uint8_t)threadIdx.x;
+      }
+      __syncthreads();
+      sorted = s_order;
+    }
+  }
   TileWalk walk;
   AttnTile t;
   bool ok = true;
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (warp < 4) {
     set_max_regs_dec<kAtRegsIssue>();
     if (warp == 0) {
-      walk.start<KEYS>(a, tile_pos);
+      walk.start(a, tile_pos, sorted);
       int kslot = 0, vslot = 0, nq = 0;
       uint32_t kphase = 0, vphase = 0;
       const int boxes = a.dim > 64 ? 2 : 1;
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         ok = __shfl_sync(~0u, ok, 0);
       }
     } else if (warp == 1) {
-      walk.start<KEYS>(a, tile_pos);
+      walk.start(a, tile_pos, sorted);
       const uint32_t idesc = idesc_bf16_f32(kAtBM, kAtBN) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);   // -Q for a negative scale
       const int ksteps = (a.dim + 15) / 16;
       const uint32_t d = uniform(tmem) + kAtColS, bars = uniform(smem_u32(full));
@@ -409,7 +420,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
       }
     } else if (warp == 2) {
-      walk.start<KEYS>(a, tile_pos);
+      walk.start(a, tile_pos, sorted);
       const uint32_t idesc = idesc_bf16_f32(kAtBM, (a.dim + 15) / 16 * 16) | (1u << 16);   // V: N-major
       const uint32_t acc = uniform(tmem), bars = uniform(smem_u32(full));
       const uint32_t v0 = desc_lo_mn(uniform(smem_u32(sKV)) + KS * Cfg::TILE, Cfg::BOX);
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   } else {
     set_max_regs_inc<kAtRegsSoftmax>();
-    walk.start<KEYS>(a, tile_pos);
+    walk.start(a, tile_pos, sorted);
     const int s = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int row_pos = row / group, row_head = row - row_pos * group;
@@ -779,12 +790,22 @@ inline CUtensorMap make_heads_tmap(const __nv_bfloat16* p, long long tokens, int
 
 template <int DP, int ROWS>
 void launch_attention_as(const AttnArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                         int splits, int sms, int out_mode, cudaStream_t s) {
+                         int sms, int out_mode, cudaStream_t s) {
   using Cfg = AttnCfg<DP, ROWS>;
   auto kern = attention_kernel<DP, ROWS>;
   allow_smem(kern, Cfg::SMEM, kAtRegs);
-  const int most = splits > 1 ? max_clusters(kern, splits, kAtThreads, Cfg::SMEM) : sms;
-  const int workers = (int)std::min<long long>(a.max_tiles * a.kv_heads, most);
+  const long long units = a.max_tiles * a.kv_heads;
+  int splits = 1, workers = (int)std::min<long long>(units, sms);
+  if (ROWS > 0) {
+    // CTAs of a cluster: those that give the shortest time if all sequences are
+    // as long as the longest, with kAtJoinBlocks blocks' time lost on each tile
+    long long best = -1;
+    for (int n = 1; n <= 8; n *= 2) {
+      const int most = n > 1 ? max_clusters(kern, n, kAtThreads, Cfg::SMEM) : sms;
+      const long long time = (units + most - 1) / most * (((long long)a.max_k + n * kAtBN - 1) / (n * kAtBN) + kAtJoinBlocks);
+      if (best < 0 || time < best) best = time, splits = n, workers = (int)std::min<long long>(units, most);
+    }
+  }
   launch_op(s, splits, kern, dim3((unsigned)(workers * splits)), dim3(kAtThreads), Cfg::SMEM, mq, mk, mv, a, splits,
             out_mode);
 }
@@ -799,11 +820,6 @@ inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
   const int rows = !keys ? 0 : group <= 16 && a.max_q <= 16 / group ? 16 : 64;
   const int half_pos = (keys ? rows : kAtBM) / group;
   a.max_tiles = tiles(keys ? half_pos : 2 * half_pos);
-  int splits = 1;
-  if (keys) {
-    const int blocks = a.max_k / kAtBN;
-    while (splits < 8 && blocks >= 4 * splits && a.max_tiles * a.kv_heads * splits < 4ll * sms) splits *= 2;
-  }
   const CUtensorMap mq = make_heads_tmap(a.q, a.total_q, a.heads, a.dim, a.q_t, a.q_h, half_pos, group);
   const bool none = a.total_k == 0;   // no key: the maps are not used, but they have to be valid
   const CUtensorMap mk = none ? mq : make_heads_tmap(a.k, a.total_k, a.kv_heads, a.dim, a.k_t, a.k_h, kAtBN, 1);
@@ -814,9 +830,9 @@ inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
   const int out_mode = rows_aligned(32) ? 2 : rows_aligned(16) ? 1 : 0;
   auto launch = [&](auto d) {
     constexpr int DP = decltype(d)::value;
-    if (rows == 16) launch_attention_as<DP, 16>(a, mq, mk, mv, splits, sms, out_mode, s);
-    else if (rows == 64) launch_attention_as<DP, 64>(a, mq, mk, mv, splits, sms, out_mode, s);
-    else launch_attention_as<DP, 0>(a, mq, mk, mv, splits, sms, out_mode, s);
+    if (rows == 16) launch_attention_as<DP, 16>(a, mq, mk, mv, sms, out_mode, s);
+    else if (rows == 64) launch_attention_as<DP, 64>(a, mq, mk, mv, sms, out_mode, s);
+    else launch_attention_as<DP, 0>(a, mq, mk, mv, sms, out_mode, s);
   };
   if (a.dim > 64) launch(std::integral_constant<int, 128>());
   else launch(std::integral_constant<int, 64>());
