@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           m[r] = fmaxf(m[r], __shfl_xor_sync(~0u, m[r], 1));
           m[r] = fmaxf(m[r], __shfl_xor_sync(~0u, m[r], 2));
         }
-        if (!wait_o()) return false;
+        wait_o();
         tc_fence_after();
         if (__any_sync(~0u, (m[0] - top2[0]) * c > 8.f || (m[1] - top2[1]) * c > 8.f)) {
           float f[2];
@@ -627,26 +627,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[s]);
-        return true;
       };
       for (int j = KEYS ? s : 0; j < t.nb; j += KEYS ? 2 : 1, ++done) {
-        ok = op_wait_warp(&sfull[s], sphase, &s_abort);
-        if (!ok) break;
+        op_wait_through(&sfull[s], sphase, &s_abort);
         sphase ^= 1u;
         // the P V of this half's previous block: it has read P and written O
         auto wait_o = [&] {
           if (done > 0) {
-            ok = op_wait_warp(&ofull[s], ophase, &s_abort);
+            op_wait_through(&ofull[s], ophase, &s_abort);
             ophase ^= 1u;
           }
-          return ok;
         };
         if constexpr (ROWS == 16) {
-          if (!few_rows(t.b0 + j, done, wait_o)) break;
+          few_rows(t.b0 + j, done, wait_o);
           continue;
         }
         if (!active) {
-          if (!wait_o()) break;
+          wait_o();
           if (lane == 0) mbar_arrive(sfree), mbar_arrive(&pfull[s]);
           __syncwarp();
           continue;
@@ -668,7 +665,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
         for (int x = 3; x + 1 < 128; x += 2) m4[(x >> 1) & 3] = max3(m4[(x >> 1) & 3], v[x], v[x + 1]);
         const float m = fmaxf(max3(m4[0], m4[1], m4[2]), fmaxf(m4[3], v[127]));
-        if (!wait_o()) break;
+        wait_o();
         tc_fence_after();
         // (an infinite difference included: the first block, or a row that saw nothing so far)
         if (__any_sync(~0u, (m - top) * c > 8.f)) {
@@ -700,10 +697,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
         sum = s0 + s1;
       }
-      if (!ok) break;
       if (done > 0) {
-        ok = op_wait_warp(&ofull[s], ophase, &s_abort);
-        if (!ok) break;
+        op_wait_through(&ofull[s], ophase, &s_abort);
         ophase ^= 1u;
         tc_fence_after();
       }
