@@ -158,28 +158,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (leader && lane == 0) {
-      int stage = 0, it = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = cid; t < total && ok; t += ncl, ++it) {
-        const int buf = it & 1;
-        ok = op_wait(&tempty[buf], ((it >> 1) & 1) ^ 1u, &s_abort);
-        if (!ok) break;
+    if (leader) {
+      const uint32_t acc = uniform(tmem), xa = desc_lo_k(uniform(smem_u32(sA))), wa = desc_lo_k(uniform(smem_u32(sB)));
+      const uint32_t empty_u = uniform(smem_u32(empty)), tfull_u = uniform(smem_u32(tfull));
+      uint32_t stage = 0, phase = 0;
+      int it = 0;
+      for (int t = cid; t < total; t += ncl, ++it) {
+        const uint32_t buf = it & 1;
+        op_wait_through(&tempty[buf], ((it >> 1) & 1) ^ 1u, &s_abort);
         tc_fence_after();
         for (int kb = 0; kb < nkb; ++kb) {
-          ok = op_wait(&full[stage], phase, &s_abort);
-          if (!ok) break;
+          op_wait_through(&full[stage], phase, &s_abort);
           tc_fence_after();
-          const uint32_t xa = smem_u32(sA + stage * Cfg::A_BYTES), wa = smem_u32(sB + stage * Cfg::B_BYTES);
+          const uint32_t xs = xa + stage * (Cfg::A_BYTES >> 4), ws = wa + stage * (Cfg::B_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16_pair(tmem + buf * BN, smem_desc_sw128(xa + k * 32), smem_desc_sw128(wa + k * 32),
-                           idesc_bf16_f32(256, BN), kb > 0 || k > 0);
-          umma_commit_pair(&empty[stage], 0x3);
+            for (int k = 0; k < 4; ++k)
+              umma_bf16_pair_lo(acc + buf * BN, xs + 2 * k, ws + 2 * k, idesc_bf16_f32(256, BN), kb > 0 || k > 0);
+            umma_commit_both_at(empty_u + 8 * stage);
+            if (kb == nkb - 1) umma_commit_both_at(tfull_u + 8 * buf);
+          }
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
-        umma_commit_pair(&tfull[buf], 0x3);
       }
     }
   } else {
@@ -202,10 +202,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
       };
       if (res) fetch(seq, n0);
-      if (!op_wait_warp(&tfull[buf], (it >> 1) & 1, &s_abort)) break;
+      op_wait_through(&tfull[buf], (it >> 1) & 1, &s_abort);
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + half * cols;
-      bool ok = true;
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++seq) {
         const int n = n0 + c * 2 * cols;
@@ -220,8 +219,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (lane == 0) mbar_arrive_cluster(tempty_l + 8u * buf);
         }
         if (res) {
-          ok = op_wait_warp(&rbar[seq & 1], (seq >> 1) & 1, &s_abort);
-          if (!ok) break;
+          op_wait_through(&rbar[seq & 1], (seq >> 1) & 1, &s_abort);
         } else {
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
@@ -279,7 +277,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         if (res && c + 1 < chunks) fetch(seq + 1, n + 2 * cols);
       }
-      if (!ok) break;
     }
     if (lane == 0) bulk_wait<0>();
   }
