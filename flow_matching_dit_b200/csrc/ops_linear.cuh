@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // Every CTA puts its partial tile into its own shared memory (f32, over the
 // spent stages); CTA r then adds the rows r, r + S, ... of all S partial tiles
 // in the order of the parts, so the result does not depend on timing, and
-// writes them with neighbouring columns on neighbouring lanes: any alignment,
-// any width.
+// writes them with neighbouring columns on neighbouring lanes, by fours where
+// alignment and width allow.
 // Rows of x that a tile does not have are not loaded: boxes of `xrows` rows; the
 // MMA reads whatever the shared memory behind them holds into accumulator rows
 // that nobody reads.
@@ -365,26 +365,28 @@ __global__ void __launch_bounds__(kSplitThreads)
       tma_load_2d(sA + stage * xbytes, &tmX, &full[stage], kb * 64, (int)m0);
       if (++stage == stages) stage = 0, phase ^= 1u;
     }
-  } else if (warp == 1 && lane == 0) {
-    int stage = 0;
-    uint32_t phase = 0;
+  } else if (warp == 1) {
+    const uint32_t acc = uniform(tmem), xa = desc_lo_k(uniform(smem_u32(sA))), wa = desc_lo_k(uniform(smem_u32(sB)));
+    const uint32_t empty_u = uniform(smem_u32(empty)), done_u = uniform(smem_u32(done));
+    uint32_t stage = 0, phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!op_wait(&full[stage], phase, &s_abort)) break;
+      op_wait_through(&full[stage], phase, &s_abort);
       tc_fence_after();
-      const uint32_t xa = smem_u32(sA + stage * xbytes), wa = smem_u32(sB + stage * wbytes);
+      const uint32_t xs = xa + stage * (xbytes >> 4), ws = wa + stage * (wbytes >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        umma_bf16(tmem, smem_desc_sw128(xa + k * 32), smem_desc_sw128(wa + k * 32), idesc_bf16_f32(128, BN),
-                  kb > kb0 || k > 0);
-      umma_commit(&empty[stage]);
+        for (int k = 0; k < 4; ++k)
+          umma_bf16_lo(acc, xs + 2 * k, ws + 2 * k, idesc_bf16_f32(128, BN), kb > kb0 || k > 0);
+        umma_commit_at(kb == kb1 - 1 ? done_u : empty_u + 8 * stage);
+      }
       if (++stage == stages) stage = 0, phase ^= 1u;
     }
-    umma_commit(done);
   }
   __syncwarp();
   // the products are complete, so every load has landed and every stage has been read
-  const bool ok = op_wait_warp(done, 0, &s_abort);
+  op_wait_through(done, 0, &s_abort);
   __syncthreads();
+  const bool ok = !s_abort;
   tc_fence_after();
   const int rows = (int)min((long long)128, a.m - m0);
   const int q = warp & 3;
@@ -407,33 +409,82 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (splits > 1) cluster_sync();
   else __syncthreads();
   if (ok) {
+    // lane: 4 columns of a row, BN / 4 lanes a row; its rows are `stride` apart.
+    // Four of them at a time, so that their reads are under way together.
+    constexpr int LANES = BN / 4, PER = 32 / LANES;
+    const int col = (lane % LANES) * 4, n = n0 + col, left = a.n - n;   // columns from here on
+    const int stride = 8 * PER * splits;
+    const int es = a.out_f32 ? 4 : 2;
+    const bool vec = left >= 4 && ((uintptr_t)a.out % (4 * es) == 0) && a.ldo % 4 == 0 &&
+                     (a.residual == nullptr || ((uintptr_t)a.residual % (4 * es) == 0 && a.ldr % 4 == 0));
+    float bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bias[e] = a.bias != nullptr && e < left ? __ldg(a.bias + n + e) : 0.f;
     uint32_t base[8];
 #pragma unroll
     for (int s = 0; s < 8; ++s) base[s] = s < splits ? (splits > 1 ? mapa_shared(part, s) : smem_u32(part)) : 0;
-    // a warp takes a row's 32 columns at a time
-    const int groups = BN / 32;
-    for (int u = warp; u < (rows - rank + splits - 1) / splits * groups; u += kSplitThreads / 32) {
-      const int row = rank + u / groups * splits, col = (u % groups) * 32 + lane, n = n0 + col;
-      const uint32_t at = (uint32_t)(row * BN + (((col >> 2) ^ (row & 7)) << 2) + (col & 3)) * 4u;
-      float part_s[8];
+    for (int r0 = rank + splits * (warp * PER + lane / LANES); r0 < rows; r0 += 4 * stride) {
+      float v[4][4], res[4][4];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s < splits) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part_s[s]) : "r"(base[s] + at));
-      float v[2] = {part_s[0], 0.f};
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + i * stride;
+        if (row >= rows || left <= 0) continue;
+        if (a.residual != nullptr) {
+          const long long at = (m0 + row) * a.ldr + n;
+          if (a.out_f32) {
+            const float* p = static_cast<const float*>(a.residual) + at;
+            if (vec) *reinterpret_cast<float4*>(res[i]) = *reinterpret_cast<const float4*>(p);
+            else
 #pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < splits) v[0] += part_s[s];
-      if (n < a.n) {
-        const long long m = m0 + row;
-        if (a.bias != nullptr) v[0] += a.bias[n];
-        apply_act(a.act, v);
-        if (a.out_f32) {
-          if (a.residual != nullptr) v[0] += static_cast<const float*>(a.residual)[m * a.ldr + n];
-          static_cast<float*>(a.out)[m * a.ldo + n] = v[0];
+              for (int e = 0; e < 4; ++e) res[i][e] = e < left ? p[e] : 0.f;
+          } else {
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.residual) + at;
+            if (vec) *reinterpret_cast<float4*>(res[i]) = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p));
+            else
+#pragma unroll
+              for (int e = 0; e < 4; ++e) res[i][e] = e < left ? __bfloat162float(p[e]) : 0.f;
+          }
+        }
+        const uint32_t at = (uint32_t)(row * BN + ((((col >> 2) ^ (row & 7))) << 2)) * 4u;
+        if (splits == 1) {
+          *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(part) + at);
         } else {
-          if (a.residual != nullptr)
-            v[0] += __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[m * a.ldr + n]);
-          static_cast<__nv_bfloat16*>(a.out)[m * a.ldo + n] = __float2bfloat16_rn(v[0]);
+          float4 f[8];
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (s < splits) f[s] = ld_cluster_f4(base[s] + at);
+          *reinterpret_cast<float4*>(v[i]) = f[0];
+#pragma unroll
+          for (int s = 1; s < 8; ++s)
+            if (s < splits) v[i][0] += f[s].x, v[i][1] += f[s].y, v[i][2] += f[s].z, v[i][3] += f[s].w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + i * stride;
+        if (row >= rows || left <= 0) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] += bias[e];
+        apply_act(a.act, v[i]);
+        if (a.residual != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][e] += res[i][e];
+        }
+        const long long at = (m0 + row) * a.ldo + n;
+        if (a.out_f32) {
+          float* p = static_cast<float*>(a.out) + at;
+          if (vec) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(v[i]);
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < left) p[e] = v[i][e];
+        } else {
+          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
+          if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < left) p[e] = __float2bfloat16_rn(v[i][e]);
         }
       }
     }
