@@ -10,6 +10,8 @@
 //                        cannot address
 #pragma once
 
+#include <atomic>
+
 #include "gemm_tc.cuh"
 #include "ops_common.cuh"
 
@@ -27,9 +29,18 @@ struct LinearArgs {
   int act;
 };
 
-// Activations in f32.  v / (1 + exp(-v)) with the fast exponential and
-// quotient: a few 2^-22 of the value, 1 + exp overflowing gives 0.
-__device__ __forceinline__ float sigmoid_times(float v, float a) { return __fdividef(v, 1.f + __expf(-a)); }
+// Activations in f32.  v0 and v1 by 1 / (1 + 2^-a) of theirs, with one reciprocal for
+// both: of the product, times the other's denominator (the special function unit is
+// what such an epilogue waits for: 16 results a cycle).  Powers are cut at 2^62, so that
+// the product stays finite: what that changes is below 2^-56 of a value.  A few 2^-22 of
+// the value otherwise.
+__device__ __forceinline__ void sigmoid_times2(float& v0, float& v1, float a0, float a1) {
+  const float d0 = 1.f + ex2(fminf(-a0, 62.f)), d1 = 1.f + ex2(fminf(-a1, 62.f));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
+  v0 *= r * d1;
+  v1 *= r * d0;
+}
 
 template <int N>
 __device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
@@ -41,11 +52,15 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
     for (int j = 0; j < N; j += 2) gelu_erf2(v[j], v[j + 1]);
   } else if (act == GDIT_ACT_GELU_TANH) {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      v[j] = sigmoid_times(v[j], 1.5957691216057308f * fmaf(0.044715f * v[j] * v[j], v[j], v[j]));
+    for (int j = 0; j < N; j += 2) {   // 2 sqrt(2 / pi) log2(e) (v + 0.044715 v^3)
+      constexpr float c = 2.3022081985104166f;
+      sigmoid_times2(v[j], v[j + 1], c * fmaf(0.044715f * v[j] * v[j], v[j], v[j]),
+                     c * fmaf(0.044715f * v[j + 1] * v[j + 1], v[j + 1], v[j + 1]));
+    }
   } else if (act == GDIT_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = sigmoid_times(v[j], v[j]);
+    for (int j = 0; j < N; j += 2)
+      sigmoid_times2(v[j], v[j + 1], 1.4426950408889634f * v[j], 1.4426950408889634f * v[j + 1]);
   }
 }
 
@@ -196,7 +211,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int buf = it & 1, ym = mi * 256 + (int)rank * 128 + q * 32, n0 = ni * BN + half * cols;
       auto fetch = [&](int s, int n) {   // residual box of chunk s
         if (lane == 0) {
-          bulk_wait_read<1>();   // the store of chunk s - 2 has left the box
+          bulk_wait_read<0>();   // the store of chunk s - 2 has left the box
           mbar_arrive_expect_tx(&rbar[s & 1], 4096);
           tma_load_2d(boxes + (s & 1) * 4096, &tmR, &rbar[s & 1], n, ym);
         }
@@ -220,6 +235,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         if (res) {
           op_wait_through(&rbar[seq & 1], (seq >> 1) & 1, &s_abort);
+          if (c + 1 < chunks) fetch(seq + 1, n + 2 * cols);
+          __syncwarp();
         } else {
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
@@ -275,7 +292,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (n < a.n && ym < a.m) tma_store_2d(&tmO, box, n, ym);   // clipped at the matrix' edges
           bulk_commit();
         }
-        if (res && c + 1 < chunks) fetch(seq + 1, n + 2 * cols);
       }
     }
     if (lane == 0) bulk_wait<0>();
@@ -301,6 +317,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // that nobody reads.
 
 constexpr int kSplitThreads = 256;
+constexpr int kSplitSmem = 226 * 1024;   // at most: the kernel has some bytes of its own
 
 struct SplitPlan {
   int bn, splits, stages, xrows;
@@ -532,24 +549,60 @@ void launch_linear_split(const LinearArgs& a, const SplitPlan& p, cudaStream_t s
   const CUtensorMap tx = make_tmap(a.x, a.m, a.k, a.ldx, p.xrows), tw = make_tmap(a.w, a.n, a.k, a.ldw, BN);
   const long long tiles = (a.m + 127) / 128 * ((a.n + BN - 1) / BN);
   REQUIRE(tiles * p.splits <= INT32_MAX, "m %lld x n %d has too many tiles", a.m, a.n);
-  allow_smem(linear_split_kernel<BN>, 226 * 1024);   // the kernel has some bytes of its own
+  allow_smem(linear_split_kernel<BN>, kSplitSmem);
   launch_op(s, p.splits, linear_split_kernel<BN>, dim3((unsigned)(tiles * p.splits)), dim3(kSplitThreads), p.smem(), tx,
             tw, a, p.splits, p.stages, p.xrows, p.smem());
 }
 
+// CTAs in clusters of 1 to 8 that the current device holds with one an SM, asked once.
+struct SplitSlots {
+  int of[9];
+};
+inline const SplitSlots& split_slots(int sms) {
+  static std::mutex mu;
+  static std::atomic<const SplitSlots*> known[kMaxDevices];
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  const SplitSlots* p = known[dev].load(std::memory_order_acquire);
+  if (p == nullptr) {
+    std::lock_guard<std::mutex> lock(mu);
+    p = known[dev].load(std::memory_order_relaxed);
+    if (p == nullptr) {
+      SplitSlots s = {{0, sms}};
+      for (int n = 2; n <= 8; ++n) s.of[n] = n * max_clusters(linear_split_kernel<128>, n, kSplitThreads, kSplitSmem);
+      p = new SplitSlots(s);
+      known[dev].store(p, std::memory_order_release);
+    }
+  }
+  return *p;
+}
+
 inline SplitPlan plan_split(long long m, int n, int k, int sms) {
-  SplitPlan p;
+  SplitPlan p = {};
+  const SplitSlots& slots = split_slots(sms);
   const int nkb = (k + 63) / 64;
   const long long mt = (m + 127) / 128;
-  auto tiles = [&](int bn) { return mt * ((n + bn - 1) / bn); };
-  // the widest tiles that still give every SM one, with K cut over up to 8 CTAs
-  p.bn = tiles(128) * std::min(8, std::max(1, nkb / 4)) >= sms ? 128 : tiles(64) * std::min(8, std::max(1, nkb / 4)) >= sms ? 64 : 32;
-  p.splits = 1;
-  while (p.splits < 8 && 2 * p.splits * 2 <= nkb && tiles(p.bn) * p.splits < sms) p.splits *= 2;
-  p.xrows = m >= 96 ? 128 : m > 32 ? 64 : 32;
-  if (m > 64) p.xrows = 128;
+  p.xrows = 8;
+  while (p.xrows < 128 && p.xrows < m) p.xrows *= 2;
+  // The tile width and the parts of K with the shortest time, in microseconds: a CTA's
+  // own (its start, its steps along K, the kilobytes it loads, its share of the tile's
+  // rows to write), times the CTAs for each place, and the join.  The coefficients fit
+  // the times of 78 sizes (1 to 2048 rows, 16 to 8192 columns, K of 32 to 8192) in up to
+  // 21 plans each; the plan chosen took 4 % longer than the best one on average, 31 % at
+  // most.
+  double best = 0;
+  const int rows = (int)std::min<long long>(m, 128);
+  for (int bn = 128; bn >= 32; bn /= 2)
+    for (int s = 1; s <= 8 && (s == 1 || 2 * s <= nkb); ++s) {
+      const int steps = (nkb + s - 1) / s;
+      const double own = 1.18 + 0.116 * steps + 0.0069 * steps * (p.xrows + bn) / 8 + 5.35 * rows * bn / 16384 / s;
+      const double places = (double)(mt * ((n + bn - 1) / bn) * s) / slots.of[s];
+      const double time = own * std::max(1.0, places) + (s > 1 ? 1.2 + 0.04 * s : 0);
+      if (p.bn == 0 || time < best) best = time, p.bn = bn, p.splits = s;
+    }
+  const long long ctas = mt * ((n + p.bn - 1) / p.bn) * p.splits;
   const int per = (nkb + p.splits - 1) / p.splits;
-  const int budget = (tiles(p.bn) * p.splits > sms ? 110 : 220) * 1024 - 2048 - (128 - p.xrows) * 128;
+  const int budget = (ctas > slots.of[p.splits] ? 110 : 220) * 1024 - 2048 - (128 - p.xrows) * 128;   // two CTAs an SM, or one
   p.stages = std::max(2, std::min({per, 16, budget / ((p.xrows + p.bn) * 128)}));
   return p;
 }
@@ -560,7 +613,12 @@ inline void launch_linear(const LinearArgs& a, int sms, cudaStream_t s) {
   const bool tma = tma_ok(a.out, a.ldo) && (a.residual == nullptr || tma_ok(a.residual, a.ldr));
   const long long mt = (a.m + 255) / 256;
   if (tma && mt * ((a.n + 127) / 128) >= sms / 2) {
-    if (mt * ((a.n + 255) / 256) >= sms / 2) launch_linear_pair<256>(a, sms, s);
+    // Rounds of tiles over the pairs times the time of a step of 64 along K, which is
+    // what a CTA loads for it (at about 51 bytes a cycle from L2) or the product:
+    // 32 KB and 512 cycles at 256 columns, 24 KB and 256 cycles at 128
+    const long long pairs = sms / 2, wide = (mt * ((a.n + 255) / 256) + pairs - 1) / pairs * 640,
+                    narrow = (mt * ((a.n + 127) / 128) + pairs - 1) / pairs * 480;
+    if (wide <= narrow) launch_linear_pair<256>(a, sms, s);
     else launch_linear_pair<128>(a, sms, s);
     return;
   }
