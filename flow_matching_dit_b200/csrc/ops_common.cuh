@@ -49,15 +49,14 @@ __device__ __forceinline__ uint2 load_b16x4(const __nv_bfloat16* p) {
 __device__ __forceinline__ bool op_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
-    if (*abort) return false;
+  while (!*abort) {
+    if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
     if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
       *abort = 1;
       atomicOr(&g_op_status, DEV_ERR_TIMEOUT);
-      return false;
     }
   }
-  return true;
+  return false;
 }
 
 // The same for a whole warp: one lane polls.

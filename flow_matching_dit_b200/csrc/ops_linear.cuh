@@ -31,15 +31,15 @@ struct LinearArgs {
 
 // Activations in f32.  v0 and v1 by 1 / (1 + 2^-a) of theirs, with one reciprocal for
 // both: of the product, times the other's denominator (the special function unit is
-// what such an epilogue waits for: 16 results a cycle).  Powers are cut at 2^62, so that
-// the product stays finite: what that changes is below 2^-56 of a value.  A few 2^-22 of
-// the value otherwise.
+// what such an epilogue waits for: 16 results a cycle).  So that the product stays
+// finite, powers are cut at 2^62, and above that the factor is 0.  Good to a few 2^-22
+// of the value otherwise.
 __device__ __forceinline__ void sigmoid_times2(float& v0, float& v1, float a0, float a1) {
   const float d0 = 1.f + ex2(fminf(-a0, 62.f)), d1 = 1.f + ex2(fminf(-a1, 62.f));
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
-  v0 *= r * d1;
-  v1 *= r * d0;
+  v0 *= -a0 > 62.f ? 0.f : r * d1;
+  v1 *= -a1 > 62.f ? 0.f : r * d0;
 }
 
 template <int N>
@@ -423,8 +423,14 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
   }
   tc_fence_before();
+  __syncthreads();
+  // given back before the CTAs of the cluster wait for one another: one of them may
+  // still be waiting for TMEM that another kernel on its SM holds
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, BN);
+  }
   if (splits > 1) cluster_sync();
-  else __syncthreads();
   if (ok) {
     // lane: 4 columns of a row, BN / 4 lanes a row; its rows are `stride` apart.
     // Four of them at a time, so that their reads are under way together.
@@ -507,11 +513,6 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
   }
   if (splits > 1) cluster_sync();   // nobody leaves while its partial tile is read
-  else __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, BN);
-  }
 }
 
 // ------------------------------------------------------------------ planning and launches

@@ -161,6 +161,44 @@ def test_linear_values_that_are_not_finite_stay_in_their_rows():
     clean()
 
 
+@pytest.mark.parametrize("m, n, k", [(1, 8192, 8192), (8, 11008, 4096), (3, 2671, 1792), (17, 1024, 1024), (33, 552, 5264),
+                                     (200, 5000, 5000), (500, 500, 4000), (1015, 85, 5008), (300, 2048, 2048), (9, 16, 8)])
+def test_linear_split_plans(m, n, k):
+    """Sizes whose plans differ: tile widths, parts of K (clusters of any size up to 8), boxes of 8 to 128 rows."""
+    check_linear(m, n, k, "silu", "bf16", True, True)
+    check_linear(m, n, k, "none", "f32", False, True)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("m", [4, 1100])
+def test_linear_activations_far_out(act, m):
+    """Arguments from tiny to far outside: out = act(z), z = the row's value, neighbours with another size in turn."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    z = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-4, -1e-4, 0.5, -0.5, 3.0, -3.0, 6.0, -6.0, 20.0, -20.0, 42.0, -42.0, 60.0,
+                      -60.0, 100.0, -100.0, 1e4, -1e4, 1e12, -1e12, 1e20, -1e20, 3e38, -3e38, 2.0, -2.0, 90.0, -90.0],
+                     device="cuda").bfloat16()
+    n, k = 1024, 64
+    x = torch.zeros(m, k, device="cuda", dtype=torch.bfloat16)
+    x[:, 0] = z.repeat(m // 32 + 1)[:m]
+    x[:, 1] = 1
+    w = torch.zeros(n, k, device="cuda", dtype=torch.bfloat16)
+    w[:, 0] = 1
+    b = torch.zeros(n, device="cuda")
+    got = linear(x, w, b, activation=act, out_dtype=torch.float32)
+    w[:, 1] = z.repeat(n // 32 + 1)[:n]          # and along the columns
+    x[:, 0] = 0
+    across = linear(x, w, b, activation=act, out_dtype=torch.float32)
+    for out, arg in ((got, z.repeat(m // 32 + 1)[:m, None].expand(m, n)), (across, z.repeat(n // 32 + 1)[None, :n].expand(m, n))):
+        v = arg.double()
+        ref = {"relu": v.clamp_min(0), "gelu": 0.5 * v * torch.erfc(-v / math.sqrt(2)),
+               "gelu_tanh": v * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)),
+               "silu": v * torch.sigmoid(v)}[act]
+        # an erf to 3e-7, exponentials and reciprocals to a few 2^-22, nothing below 2^-62 of the argument
+        within(out, ref, 2.0 ** -19 * ref.abs() + 4e-7 * v.abs().clamp_max(8) + 2.0 ** -61 * v.abs().clamp_max(64) + 1e-30, act)
+    clean()
+
+
 def test_linear_refusals():
     import torch
     from flow_matching_dit_b200 import GditError, linear
@@ -490,6 +528,29 @@ def test_attention_single_token(kl, heads, kv_heads, dim):
     check_attention([1] * len(kl), kl, heads=heads, kv_heads=kv_heads, dim=dim, slot=max(kl) + 1)
 
 
+@pytest.mark.parametrize("batch", [255, 256, 257, 700])
+def test_attention_many_sequences(batch):
+    """Single tokens of more sequences than are taken by falling length, and of as many."""
+    kl = [int(x) for x in np.random.RandomState(batch).randint(0, 300, batch)]
+    check_attention([1] * batch, kl, 4, 2, 64, slot=300)
+    check_attention([i % 3 for i in range(batch)], [min(i % 3, n) + n for i, n in enumerate(kl)], 2, 1, 64)
+
+
+@pytest.mark.parametrize("heads, kv_heads", [(16, 1), (17, 1), (32, 1), (64, 1), (65, 1), (128, 1), (96, 2)])
+@pytest.mark.parametrize("nq", [1, 4])
+def test_attention_wide_groups(heads, kv_heads, nq):
+    """Tiles of 16, 64 and 128 rows, full and nearly empty."""
+    check_attention([nq] * 3, [700, nq, 129 + nq], heads, kv_heads, 64, slot=705)
+
+
+@pytest.mark.parametrize("heads, kv_heads, dim", [(2, 1, 128), (7, 1, 64), (12, 4, 80), (5, 5, 40)])
+@pytest.mark.parametrize("ql, kl", [([300], [5000]), ([70, 1, 64], [3000, 400, 64]), ([129], [129]), ([65, 0, 200], [65, 7, 300])])
+def test_attention_few_tiles(heads, kv_heads, dim, ql, kl):
+    """Too few tiles for the SMs: parts of the keys, joined over clusters."""
+    for causal in (True, False):
+        check_attention(ql, kl, heads, kv_heads, dim, causal)
+
+
 @pytest.mark.parametrize("nq", [2, 3, 5, 8, 16, 33])
 def test_attention_few_tokens(nq):
     """The tokens of a draft, checked in one call."""
@@ -716,6 +777,60 @@ def test_two_streams_at_once():
     for g, w in zip(got, want):
         assert all(torch.equal(t, w) for t in g)
     clean()
+
+
+def test_captured_graphs_side_by_side():
+    """Two captured graphs replay on two streams at once, again and again, with new inputs: nothing is shared."""
+    import torch
+    from flow_matching_dit_b200 import attention, linear, norm_residual
+    g = gen(11)
+    bf = torch.bfloat16
+    cu = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = [rnd(g, 4096, 2, 128, dtype=bf) for _ in range(2)]
+    w1, w2, gain = rnd(g, 1024, 1024, std=0.03, dtype=bf), rnd(g, 1024, 1024, std=0.03, dtype=bf), rnd(g, 1024)
+    cq, ck, kl = cu(0, 1, 2), cu(0, 2048, 4096), cu(2048, 1500)
+
+    def step(x):
+        h, u = norm_residual(x, None, pre="rms", pre_gain=gain, u_dtype=bf)
+        q = linear(u, w1, activation="silu").view(2, 8, 128)
+        o = attention(q, *cache, cq, ck, max_q=1, max_k=2048, k_len=kl).view(2, 1024)
+        return linear(o, w2, residual=h, out_dtype=torch.float32)
+
+    xs = [[rnd(g, 2, 1024) for _ in range(5)] for _ in range(2)]
+    want = [[step(x) for x in row] for row in xs]
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for st in streams:
+        x = torch.zeros(2, 1024, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            y = step(x)
+        graphs.append((graph, x, y))
+    got = [[], []]
+    for i in range(5):
+        for s, (st, (graph, x, y)) in enumerate(zip(streams, graphs)):
+            with torch.cuda.stream(st):
+                x.copy_(xs[s][i])
+                graph.replay()
+                got[s].append(y.clone())
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, r) for p, r in zip(a, b))
+    clean()
+
+
+def test_on_a_stream_of_its_own_and_by_handle():
+    import torch
+    from flow_matching_dit_b200 import linear, op_status
+    g = gen(12)
+    x, w = (rnd(g, 64, 256, dtype=torch.bfloat16) for _ in range(2))
+    want = linear(x, w)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    out = torch.zeros_like(want)
+    linear(x, w, out=out, stream=st.cuda_stream)
+    st.synchronize()
+    assert torch.equal(out, want) and op_status(stream=st.cuda_stream) == 0
 
 
 def test_same_bits_every_time():
