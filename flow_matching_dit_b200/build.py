@@ -1,8 +1,10 @@
 """In-tree build of the CUDA library ``libgdit.so`` for sm_100a.
 
 ``python -m flow_matching_dit_b200.build`` (or ``build()``) compiles
-``csrc/gdit.cu`` (the action head) and ``csrc/ops.cu`` (the operators) with nvcc into ``flow_matching_dit_b200/libgdit.so``, and
-with ``checked=True`` into ``libgdit_checked.so``, the range-checked build
+``csrc/gdit.cu`` (the action head) and ``csrc/ops.cu`` (the operators) with nvcc
+into ``flow_matching_dit_b200/libgdit.so``, and ``csrc/binding.cpp`` (the
+operators' Python calls) with the host compiler against torch's headers into
+``_binding.so``.  With ``checked=True`` the library goes into ``libgdit_checked.so``, the range-checked build
 (``-DGDIT_CHECKED=1``: guard bands around device allocations, index checks in
 the kernels).  nvcc cross-compiles, so this works on a machine without a GPU.
 """
@@ -18,6 +20,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdit.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = os.path.join(PKG, "csrc", "binding.cpp")
 LIB_CHECKED = os.path.join(PKG, "libgdit_checked.so")
 SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")) + glob.glob(os.path.join(PKG, "csrc", "*.cuh")))
 HEADER = os.path.join(ROOT, "include", "gdit.h")
@@ -37,6 +41,27 @@ def command(out: str = LIB, checked: bool = False) -> list:
         ["--threads", "2", "-o", out, os.path.join(PKG, "csrc", "gdit.cu"), os.path.join(PKG, "csrc", "ops.cu")]
 
 
+def binding_command(out: str = BINDING) -> list:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"), os.path.join(ROOT, "include"),
+               sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + ["-I" + p for p in include] + \
+        [BINDING_SOURCE, "-o", out, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+         "-lc10_cuda", "-lc10"]
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(s) <= t for s in (BINDING_SOURCE, HEADER))
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
@@ -44,19 +69,25 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(s) <= t for s in SOURCES + [HEADER])
 
 
-def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
-    LIB_OUT = LIB_CHECKED if checked else LIB
-    if not force and up_to_date(LIB_OUT):
-        return LIB_OUT
-    tmp = LIB_OUT + ".tmp"
-    cmd = command(tmp, checked)
+def _run(cmd: list, tmp: str, out: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    os.replace(tmp, LIB_OUT)
-    return LIB_OUT
+        raise RuntimeError(f"{cmd[0]} failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, out)
+
+
+def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
+    """Builds what is not up to date; returns the library's path."""
+    out = LIB_CHECKED if checked else LIB
+    if force or not up_to_date(out):
+        tmp = out + ".tmp"
+        _run(command(tmp, checked), tmp, out, verbose)
+    if force or not binding_up_to_date():
+        tmp = BINDING + ".tmp"
+        _run(binding_command(tmp), tmp, BINDING, verbose)
+    return out
 
 
 if __name__ == "__main__":
