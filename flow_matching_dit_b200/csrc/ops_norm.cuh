@@ -28,12 +28,17 @@ struct NormArgs {
 // hide its latency.  What bounds it: memory (h and y in, h' and u out).
 // A warp of the team takes 128 * NU neighbouring values, so that a thread's
 // addresses differ by constants:
-//   VEC   lane i holds the 4-value units i, i + 32, ...: 16 bytes of f32 or 8 of bf16
-//   else  the values i, i + 32, ...: any width and alignment
+//   kUnits    lane i holds the 4-value units i, i + 32, ...: 16 bytes of f32 or 8 of bf16
+//   kShifted  the same for a width that is no multiple of 4: the units lie where the addresses are aligned, and those
+//             that the row has only a part of, at its ends, are read and written value by value
+//   kValues   lane i holds the values i, i + 32, ...: any alignment
 // Mean and variance are sums over the registers, the second of squared deviations
 // from the first: no cancellation when the mean is large.
-template <bool VEC, int NU>
+enum RowLayout { kUnits, kShifted, kValues };
+
+template <RowLayout LAYOUT, int NU>
 struct RowTeam {
+  static constexpr bool VEC = LAYOUT != kValues;
   static constexpr int N = 4 * NU;
   int first, left;   // first value of this thread; values of the row from there on
   int warp, warps, bar;
@@ -43,7 +48,12 @@ struct RowTeam {
   __device__ __forceinline__ static constexpr int offset(int e) {   // of value e from the first
     return VEC ? (e >> 2) * 128 + (e & 3) : e * 32;
   }
-  __device__ __forceinline__ bool there(int e) const { return offset(e) < left; }
+  __device__ __forceinline__ bool there(int e) const {
+    return offset(e) < left && (LAYOUT != kShifted || first + offset(e) >= 0);
+  }
+  // the unit of value e, a multiple of 4: all in the row, or at least a part of it
+  __device__ __forceinline__ bool whole(int e) const { return LAYOUT != kShifted ? there(e) : there(e) && there(e + 3); }
+  __device__ __forceinline__ bool some(int e) const { return offset(e) < left && first + offset(e) > -4; }
 
   __device__ __forceinline__ void load(const void* p, long long base, int f32, float (&v)[N]) const {
     if (VEC) {
@@ -52,7 +62,12 @@ struct RowTeam {
 #pragma unroll
         for (int c = 0; c < N; c += 4) {
           float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (there(c)) f = load_f32x4(q + offset(c));
+          if (whole(c)) {
+            f = load_f32x4(q + offset(c));
+          } else if (LAYOUT == kShifted && some(c)) {
+            f.x = there(c) ? q[offset(c)] : 0.f, f.y = there(c + 1) ? q[offset(c + 1)] : 0.f;
+            f.z = there(c + 2) ? q[offset(c + 2)] : 0.f, f.w = there(c + 3) ? q[offset(c + 3)] : 0.f;
+          }
           v[c] = f.x, v[c + 1] = f.y, v[c + 2] = f.z, v[c + 3] = f.w;
         }
       } else {
@@ -61,7 +76,15 @@ struct RowTeam {
 #pragma unroll
         for (int c = 0; c < N; c += 4) {
           w[c >> 2] = make_uint2(0, 0);
-          if (there(c)) w[c >> 2] = load_b16x4(q + offset(c));
+          if (whole(c)) {
+            w[c >> 2] = load_b16x4(q + offset(c));
+          } else if (LAYOUT == kShifted && some(c)) {
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              b[e] = there(c + e) ? (uint32_t)reinterpret_cast<const unsigned short*>(q)[offset(c + e)] : 0u;
+            w[c >> 2] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+          }
         }
 #pragma unroll
         for (int c = 0; c < N; c += 4) {
@@ -85,28 +108,37 @@ struct RowTeam {
       float* q = static_cast<float*>(p) + base + first;
 #pragma unroll
       for (int e = 0; e < N; e += VEC ? 4 : 1) {
-        if (!there(e)) continue;
-        if (VEC) *reinterpret_cast<float4*>(q + offset(e)) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        else q[offset(e)] = v[e];
+        if (VEC && whole(e)) {
+          *reinterpret_cast<float4*>(q + offset(e)) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else if (LAYOUT != kUnits) {
+#pragma unroll
+          for (int k = 0; k < (VEC ? 4 : 1); ++k)
+            if (there(e + k)) q[offset(e + k)] = v[e + k];
+        }
       }
     } else {
       __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + base + first;
 #pragma unroll
       for (int e = 0; e < N; e += VEC ? 4 : 1) {
-        if (!there(e)) continue;
-        if (VEC) *reinterpret_cast<uint2*>(q + offset(e)) = make_uint2(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]));
-        else q[offset(e)] = __float2bfloat16_rn(v[e]);
+        if (VEC && whole(e)) {
+          *reinterpret_cast<uint2*>(q + offset(e)) = make_uint2(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]));
+        } else if (LAYOUT != kUnits) {
+#pragma unroll
+          for (int k = 0; k < (VEC ? 4 : 1); ++k)
+            if (there(e + k)) q[offset(e + k)] = __float2bfloat16_rn(v[e + k]);
+        }
       }
     }
   }
 
   // v = v * (one + a) + b with per-channel f32 vectors (NULL: one = 0, a = 1; b = 0)
   __device__ __forceinline__ void affine(float (&v)[N], const float* a, const float* b, float one) const {
+    constexpr int STEP = LAYOUT == kUnits ? 4 : 1;
     if (a != nullptr) {
 #pragma unroll
-      for (int e = 0; e < N; e += VEC ? 4 : 1) {
+      for (int e = 0; e < N; e += STEP) {
         if (!there(e)) continue;
-        if (VEC) {
+        if (STEP == 4) {
           const float4 f = *reinterpret_cast<const float4*>(a + first + offset(e));
           v[e] *= one + f.x, v[e + 1] *= one + f.y, v[e + 2] *= one + f.z, v[e + 3] *= one + f.w;
         } else {
@@ -116,9 +148,9 @@ struct RowTeam {
     }
     if (b != nullptr) {
 #pragma unroll
-      for (int e = 0; e < N; e += VEC ? 4 : 1) {
+      for (int e = 0; e < N; e += STEP) {
         if (!there(e)) continue;
-        if (VEC) {
+        if (STEP == 4) {
           const float4 f = *reinterpret_cast<const float4*>(b + first + offset(e));
           v[e] += f.x, v[e + 1] += f.y, v[e + 2] += f.z, v[e + 3] += f.w;
         } else {
@@ -166,22 +198,27 @@ struct RowTeam {
 
 constexpr int kNormThreads = 512;   // most threads of a CTA
 
-template <bool VEC, int NU>
+template <RowLayout LAYOUT, int NU>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, int warps, int teams) {
   __shared__ float red[kNormThreads / 32 * 2];
   const int which = threadIdx.x / (32 * warps);
-  RowTeam<VEC, NU> T;
+  RowTeam<LAYOUT, NU> T;
   T.warps = warps;
   T.warp = (threadIdx.x >> 5) - which * warps;
-  T.first = T.warp * 128 * NU + (threadIdx.x & 31) * (VEC ? 4 : 1);
+  T.first = T.warp * 128 * NU + (threadIdx.x & 31) * (T.VEC ? 4 : 1);
   T.left = a.dim - T.first;
   T.bar = 1 + which;
   T.red = red + which * warps * 2;
   T.which = 0;
   const float dim = (float)a.dim;
+  const int first = T.first;
   pdl_wait();
   pdl_launch_dependents();
   for (long long r = (long long)blockIdx.x * teams + which; r < a.rows; r += (long long)gridDim.x * teams) {
+    if (LAYOUT == kShifted) {
+      T.first = first - (int)((r * a.ldh) & 3);
+      T.left = a.dim - T.first;
+    }
     float h[4 * NU], y[4 * NU];
     T.load(a.h, r * a.ldh, a.h_f32, h);
     if (a.y != nullptr) T.load(a.y, r * a.ldy, a.y_f32, y);
@@ -191,7 +228,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, in
                                     (a.mod_groups > 1 && g >= a.mod_groups));
     if (bad) {
       g = 0;
-      if (T.first == 0) atomicOr(&g_op_status, OP_ERR_GROUP);
+      if (first == 0) atomicOr(&g_op_status, OP_ERR_GROUP);
     }
     const long long go = a.gate_groups > 1 ? g * a.dim : 0, mo = a.mod_groups > 1 ? g * a.dim : 0;
     if (a.y != nullptr) {
@@ -214,32 +251,35 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, in
 }
 
 inline void launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
-  auto aligned = [&](const void* p, long long ld, int f32) {   // units of 4 values
-    const int bytes = f32 ? 16 : 8;
-    return p == nullptr || ((uintptr_t)p % bytes == 0 && (ld * (f32 ? 4 : 2)) % bytes == 0);
+  auto aligned = [&](const void* p, long long ld, int f32) {   // rows that units of 4 values fit, all shifted alike
+    return p == nullptr || ((uintptr_t)p % (f32 ? 16 : 8) == 0 && (ld - a.ldh) % 4 == 0);
   };
-  bool vec = a.dim % 4 == 0 && aligned(a.h, a.ldh, a.h_f32) && aligned(a.y, a.ldy, a.y_f32) &&
-             aligned(a.out_h, a.ldoh, a.h_f32) && aligned(a.out_u, a.ldou, a.u_f32);
+  const bool units = aligned(a.h, a.ldh, a.h_f32) && aligned(a.y, a.ldy, a.y_f32) &&
+                     aligned(a.out_h, a.ldoh, a.h_f32) && aligned(a.out_u, a.ldou, a.u_f32) &&
+                     (a.dim % 4 == 0 || a.dim + 3 <= 32 * kNormThreads);   // (and with the shift the widest team holds them)
+  bool vec = units && a.dim % 4 == 0 && a.ldh % 4 == 0;
   for (const float* p : {a.post_gain, a.post_bias, a.gate, a.pre_gain, a.pre_bias, a.scale, a.shift})
     vec = vec && ((uintptr_t)p & 15u) == 0;
+  const int width = a.dim + (units && !vec && a.dim % 4 != 0 ? 3 : 0);   // with what the shift may add in front
   // Warps of a row: as few as hold it with 32 values a thread, so that a row of
   // up to 1024 needs no barrier; more where the rows leave the SMs without warps.
-  int warps = (a.dim + 1023) / 1024;
-  while (a.rows * warps < 8ll * sms && 128 * warps < a.dim && warps < 8) warps *= 2;
-  const int units = (a.dim + 128 * warps - 1) / (128 * warps);   // of 4 values a thread
+  int warps = (width + 1023) / 1024;
+  while (a.rows * warps < 8ll * sms && 128 * warps < width && warps < 8) warps *= 2;
+  const int per = (width + 128 * warps - 1) / (128 * warps);   // units of 4 values a thread
   const int teams = std::max(1, 8 / warps);
   const dim3 grid((unsigned)std::min<long long>((a.rows + teams - 1) / teams, INT32_MAX)), block(32 * warps * teams);
   auto launch = [&](auto kern) { launch_op(s, 1, kern, grid, block, 0, a, warps, teams); };
-  auto pick = [&](auto v) {
-    constexpr bool V = decltype(v)::value;
-    if (units == 1) launch(norm_kernel<V, 1>);
-    else if (units == 2) launch(norm_kernel<V, 2>);
-    else if (units <= 4) launch(norm_kernel<V, 4>);
-    else if (units <= 6) launch(norm_kernel<V, 6>);
+  auto pick = [&](auto layout) {
+    constexpr RowLayout V = decltype(layout)::value;
+    if (per == 1) launch(norm_kernel<V, 1>);
+    else if (per == 2) launch(norm_kernel<V, 2>);
+    else if (per <= 4) launch(norm_kernel<V, 4>);
+    else if (per <= 6) launch(norm_kernel<V, 6>);
     else launch(norm_kernel<V, 8>);
   };
-  if (vec) pick(std::true_type());
-  else pick(std::false_type());
+  if (vec) pick(std::integral_constant<RowLayout, kUnits>());
+  else if (units) pick(std::integral_constant<RowLayout, kShifted>());
+  else pick(std::integral_constant<RowLayout, kValues>());
 }
 
 }  // namespace gdit

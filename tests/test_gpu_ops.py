@@ -307,6 +307,31 @@ def test_norm_sizes(rows, dim):
     check_norm(rows, dim, post="layer", pre="rms", gate=1, mod=1)
 
 
+@pytest.mark.parametrize("dim", [3, 5, 6, 127, 129, 1022, 1023, 1025, 1337, 2047, 4099, 16381, 16382, 16383])
+@pytest.mark.parametrize("h, y, u", [("bf16", "bf16", "bf16"), ("f32", "bf16", "f32")])
+def test_norm_widths_that_shift_the_rows(dim, h, y, u):
+    """Rows that begin at every offset from an aligned address, with few rows and with many."""
+    for rows in (9, 1300 if dim < 5000 else 300):
+        check_norm(rows, dim, "rms", "layer", 1, 1, h=h, y=y, u=u)
+    check_norm(40, dim, "layer", "rms", 7, 7, h=h, y=y, u=u)
+
+
+def test_norm_strides_that_differ_between_the_matrices():
+    """One matrix's rows shifted, the others' not: no common layout, value by value."""
+    import torch
+    from flow_matching_dit_b200 import norm_residual
+    g = gen(5)
+    wide = rnd(g, 50, 517)
+    y = rnd(g, 50, 512, dtype=torch.bfloat16)
+    for h in (wide[:, :512], wide[:, 1:513], wide[:, 4:516]):
+        out_h, out_u = torch.zeros(50, 515, device="cuda")[:, 3:], torch.zeros(50, 514, device="cuda", dtype=torch.bfloat16)[:, :512]
+        want = norm_residual(h.contiguous(), y, pre="layer")
+        got = norm_residual(h, y, pre="layer", out_h=out_h, out_u=out_u)
+        for a, b in zip(got, want):   # the sums run in another order
+            assert torch.allclose(a.float(), b.float(), rtol=2 ** -8, atol=1e-6)
+    clean()
+
+
 @pytest.mark.parametrize("post", [None, "layer", "rms"])
 @pytest.mark.parametrize("pre", [None, "layer", "rms"])
 @pytest.mark.parametrize("gate, mod", [(0, 0), (1, 0), (0, 1), (5, 5), (1, 3), (3, 1)])
@@ -816,6 +841,29 @@ def test_captured_graphs_side_by_side():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(p, r) for p, r in zip(a, b))
+    clean()
+
+
+def test_binding_refusals():
+    import torch
+    from flow_matching_dit_b200 import attention, linear, norm_residual
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    q, cu = x.view(8, 1, 64), torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    for f, err in ((lambda: linear(x, 1), TypeError), (lambda: linear(x, None), TypeError),
+                   (lambda: linear(x, x, activation=3), ValueError), (lambda: linear(x, x, out_dtype="bf16"), TypeError),
+                   (lambda: linear(x, x, torch.zeros(8, dtype=torch.float64, device="cuda")), TypeError),
+                   (lambda: linear(x, x, torch.zeros(16, device="cuda")[::2]), TypeError),
+                   (lambda: linear(x, x, stream="0"), TypeError),
+                   (lambda: norm_residual(x, eps="no", pre="rms"), TypeError), (lambda: norm_residual(x, x, gate=3.0), TypeError),
+                   (lambda: norm_residual(x, x, row_group=torch.zeros(8, device="cuda")), TypeError),
+                   (lambda: norm_residual(x, x, pre="rms", eps=-1.0), RuntimeError),
+                   (lambda: attention(q, q, q, cu, cu, max_q=1 << 40, max_k=8), ValueError),
+                   (lambda: attention(q, q, q, cu, cu, max_q=1.5, max_k=8), TypeError),
+                   (lambda: attention(q, q, q, cu, cu, max_q=8, max_k=8, scale="x"), TypeError),
+                   (lambda: attention(q, q, q, cu, cu, max_q=8, max_k=8, k_len=cu), ValueError),
+                   (lambda: attention(q, q, q, cu[:0], cu, max_q=8, max_k=8), ValueError)):
+        with pytest.raises(err):
+            f()
     clean()
 
 
