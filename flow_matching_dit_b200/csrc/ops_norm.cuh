@@ -196,10 +196,13 @@ struct RowTeam {
   }
 };
 
-constexpr int kNormThreads = 512;   // most threads of a CTA
+constexpr int kNormThreads = 512;   // most threads of a row's team
 
-template <RowLayout LAYOUT, int NU>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a, int warps, int teams) {
+// THREADS: most of a CTA, 256 or, for rows that need a wider team, 512.  Three CTAs of
+// 256 an SM (four where the values are few) hide the latency of a row better than two
+// with all the registers they would like (2999 x 1337: 20 us instead of 24).
+template <RowLayout LAYOUT, int NU, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NU >= 6 ? 3 : 4) norm_kernel(const NormArgs a, int warps, int teams) {
   __shared__ float red[kNormThreads / 32 * 2];
   const int which = threadIdx.x / (32 * warps);
   RowTeam<LAYOUT, NU> T;
@@ -262,20 +265,22 @@ inline void launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
     vec = vec && ((uintptr_t)p & 15u) == 0;
   const int width = a.dim + (units && !vec && a.dim % 4 != 0 ? 3 : 0);   // with what the shift may add in front
   // Warps of a row: as few as hold it with 32 values a thread, so that a row of
-  // up to 1024 needs no barrier; more where the rows leave the SMs without warps.
+  // up to 1024 needs no barrier; more where the rows would leave an SM fewer than 32
+  // (4352 x 1024: 14 us in two warps a row, 20 in one, 19 in four).
   int warps = (width + 1023) / 1024;
-  while (a.rows * warps < 8ll * sms && 128 * warps < width && warps < 8) warps *= 2;
+  while (a.rows * warps < 32ll * sms && 128 * warps < width && warps < 8) warps *= 2;
   const int per = (width + 128 * warps - 1) / (128 * warps);   // units of 4 values a thread
   const int teams = std::max(1, 8 / warps);
   const dim3 grid((unsigned)std::min<long long>((a.rows + teams - 1) / teams, INT32_MAX)), block(32 * warps * teams);
   auto launch = [&](auto kern) { launch_op(s, 1, kern, grid, block, 0, a, warps, teams); };
   auto pick = [&](auto layout) {
     constexpr RowLayout V = decltype(layout)::value;
-    if (per == 1) launch(norm_kernel<V, 1>);
-    else if (per == 2) launch(norm_kernel<V, 2>);
-    else if (per <= 4) launch(norm_kernel<V, 4>);
-    else if (per <= 6) launch(norm_kernel<V, 6>);
-    else launch(norm_kernel<V, 8>);
+    if (warps > 8) launch(norm_kernel<V, 8, 512>);
+    else if (per == 1) launch(norm_kernel<V, 1, 256>);
+    else if (per == 2) launch(norm_kernel<V, 2, 256>);
+    else if (per <= 4) launch(norm_kernel<V, 4, 256>);
+    else if (per <= 6) launch(norm_kernel<V, 6, 256>);
+    else launch(norm_kernel<V, 8, 256>);
   };
   if (vec) pick(std::integral_constant<RowLayout, kUnits>());
   else if (units) pick(std::integral_constant<RowLayout, kShifted>());
