@@ -198,11 +198,11 @@ struct RowTeam {
 
 constexpr int kNormThreads = 512;   // most threads of a row's team
 
-// THREADS: most of a CTA, 256 or, for rows that need a wider team, 512.  Three CTAs of
-// 256 an SM (four where the values are few) hide the latency of a row better than two
-// with all the registers they would like (2999 x 1337: 20 us instead of 24).
+// THREADS: most of a CTA, 256 or, for rows that need a wider team, 512.  As many CTAs an
+// SM as the registers of h, y and their addresses allow without spilling (2, 3 or 4): with
+// all the registers the compiler likes, 2999 x 1337 took 24 us instead of 20.
 template <RowLayout LAYOUT, int NU, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NU >= 6 ? 3 : 4) norm_kernel(const NormArgs a, int warps, int teams) {
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NU == 8 ? 2 : NU == 6 ? 3 : 4) norm_kernel(const NormArgs a, int warps, int teams) {
   __shared__ float red[kNormThreads / 32 * 2];
   const int which = threadIdx.x / (32 * warps);
   RowTeam<LAYOUT, NU> T;
