@@ -501,54 +501,62 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     };
     if (KEYS && (warp & 2)) {
       // join: the parts (two of each CTA) of some rows, added up in their order
-      const int w = s * 2 + (warp & 1), parts = 2 * splits;
+      const int w = s * 2 + (warp & 1), parts = 2 * splits, lparts = 31 - __clz(parts);   // (powers of two)
       for (long long round = 0;
            walk.at<KEYS>(a, tile_pos, snake(round, worker, workers), rank, splits, t); ++round) {
         ok = op_wait_warp_cluster(jfull, tphase, &s_abort);
         if (!ok) break;
         tphase ^= 1u;
+        // The warp's rows are rank + splits (w + 4 j).  Item e = j * parts + p is part p of row j, 32 items at most
+        // (64 rows over 4 warps and the CTAs, two parts from each of these), and lane e looks after the statistics of item e.
         const int rows = t.np * group;
-        for (int i = rank + splits * w; i < rows; i += splits * 4) {
-          float2 st = make_float2(-INFINITY, 0.f);   // lane: of part `lane`
-          if (lane < parts) st = ld_cluster_f2(mapa_shared(stats + (lane & 1) * ROWS + i, lane >> 1));
-          float m = st.x;
+        auto row_of = [&](int e) { return rank + splits * (w + 4 * (e >> lparts)); };
+        const int i = row_of(lane);
+        const bool mine = i < rows;
+        const int items = __popc(__ballot_sync(~0u, mine));
+        float2 st = make_float2(-INFINITY, 0.f);
+        if (mine) st = ld_cluster_f2(mapa_shared(stats + (lane & 1) * ROWS + i, (lane & (parts - 1)) >> 1));
+        float m = st.x;
+        for (int o = 1; o < parts; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
+        float l = f == 0.f ? 0.f : st.y * f;
+        for (int o = 1; o < parts; o <<= 1) l += __shfl_xor_sync(~0u, l, o);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int ip = i / group, head = t.kvh * group + i - ip * group;
+        const long long token = t.s.q0 + t.p0 + ip, at = token * a.o_t + head * a.o_h;
+        if (mine && (lane & (parts - 1)) == 0 && a.lse != nullptr)
+          a.lse[token * a.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int e0 = 0; e0 < items; e0 += 8) {   // eight reads of another CTA's memory under way together
+          float4 h[8];
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-          m = __shfl_sync(~0u, m, 0);
-          const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
-          float l = st.y * f;
-          if (f == 0.f) l = 0.f;
+          for (int u = 0; u < 8; ++u) {
+            const int e = e0 + u, p = e & (parts - 1), r = row_of(e);
+            if (e < items && lane * 4 < DP)
+              h[u] = ld_cluster_f4(mapa_shared(part + (p & 1) * ROWS * DP, p >> 1) + (uint32_t)(r * DP * 4 + ((lane ^ (r & 7)) << 4)));
+          }
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-          l = __shfl_sync(~0u, l, 0);
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          const uint32_t at = (uint32_t)(i * DP * 4 + ((lane ^ (i & 7)) << 4));
-          for (int p0 = 0; p0 < parts; p0 += 2) {
-            float4 h[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              if (lane * 4 < DP) h[p] = ld_cluster_f4(mapa_shared(part + p * ROWS * DP, p0 >> 1) + at);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const float fp = __shfl_sync(~0u, f, p0 + p);
-              if (fp != 0.f && lane * 4 < DP)   // a part without keys holds nothing
-                o.x = fmaf(h[p].x, fp, o.x), o.y = fmaf(h[p].y, fp, o.y), o.z = fmaf(h[p].z, fp, o.z), o.w = fmaf(h[p].w, fp, o.w);
+          for (int u = 0; u < 8; ++u) {
+            const int e = min(e0 + u, 31);
+            const float fe = __shfl_sync(~0u, f, e);
+            if (e0 + u >= items) break;
+            if (fe != 0.f && lane * 4 < DP)   // a part without keys holds nothing
+              o.x = fmaf(h[u].x, fe, o.x), o.y = fmaf(h[u].y, fe, o.y), o.z = fmaf(h[u].z, fe, o.z), o.w = fmaf(h[u].w, fe, o.w);
+            if ((e & (parts - 1)) == parts - 1) {   // the row's last part
+              const float s = __shfl_sync(~0u, inv, e);
+              __nv_bfloat16* dst = a.out + __shfl_sync(~0u, at, e) + lane * 4;
+              if (lane * 4 < a.dim) {
+                if (out_mode > 0) {
+                  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
+                } else {
+                  dst[0] = __float2bfloat16_rn(o.x * s), dst[1] = __float2bfloat16_rn(o.y * s);
+                  dst[2] = __float2bfloat16_rn(o.z * s), dst[3] = __float2bfloat16_rn(o.w * s);
+                }
+              }
+              o = make_float4(0.f, 0.f, 0.f, 0.f);
             }
           }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const int ip = i / group, head = t.kvh * group + i - ip * group;
-          const long long token = t.s.q0 + t.p0 + ip;
-          __nv_bfloat16* dst = a.out + token * a.o_t + head * a.o_h + lane * 4;
-          if (lane * 4 < a.dim) {
-            if (out_mode > 0) {
-              *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            } else {
-              dst[0] = __float2bfloat16_rn(o.x * inv), dst[1] = __float2bfloat16_rn(o.y * inv);
-              dst[2] = __float2bfloat16_rn(o.z * inv), dst[3] = __float2bfloat16_rn(o.w * inv);
-            }
-          }
-          if (lane == 0 && a.lse != nullptr)
-            a.lse[token * a.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
         }
         __syncwarp();
         if (lane < splits) mbar_arrive_cluster(mapa_shared(jempty, lane));
