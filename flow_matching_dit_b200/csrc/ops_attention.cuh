@@ -198,9 +198,6 @@ struct TileWalk {
 // kAtSorted sequences by falling number of keys, so that the last tiles to be handed
 // out are short.
 constexpr int kAtSorted = 256;
-// What a tile of the keys kernel costs beside its blocks (its first scores, its
-// last output, the join), in blocks.
-constexpr int kAtJoinBlocks = 2;
 
 // Position r of a walk over `count` workers in rounds that run back and forth:
 // with tiles of falling length everybody gets as much.
@@ -526,38 +523,57 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const long long token = t.s.q0 + t.p0 + ip, at = token * a.o_t + head * a.o_h;
         if (mine && (lane & (parts - 1)) == 0 && a.lse != nullptr)
           a.lse[token * a.heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int nj = (int)uniform(items >> lparts);
+        auto add_up = [&](auto lp) {   // for 2, 4, 8, 16 parts: eight reads under way together, no branches between them
+          constexpr int LP = decltype(lp)::value, P = 1 << LP, R = P < 8 ? 8 / P : 1, PB = P < 8 ? P : 8;
 #pragma unroll 1
-        for (int e0 = 0; e0 < items; e0 += 8) {   // eight reads of another CTA's memory under way together
-          float4 h[8];
+          for (int j0 = 0; j0 < nj; j0 += R) {
+            float4 o[R];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int e = e0 + u, p = e & (parts - 1), r = row_of(e);
-            if (e < items && lane * 4 < DP)
-              h[u] = ld_cluster_f4(mapa_shared(part + (p & 1) * ROWS * DP, p >> 1) + (uint32_t)(r * DP * 4 + ((lane ^ (r & 7)) << 4)));
-          }
+            for (int r = 0; r < R; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int e = min(e0 + u, 31);
-            const float fe = __shfl_sync(~0u, f, e);
-            if (e0 + u >= items) break;
-            if (fe != 0.f && lane * 4 < DP)   // a part without keys holds nothing
-              o.x = fmaf(h[u].x, fe, o.x), o.y = fmaf(h[u].y, fe, o.y), o.z = fmaf(h[u].z, fe, o.z), o.w = fmaf(h[u].w, fe, o.w);
-            if ((e & (parts - 1)) == parts - 1) {   // the row's last part
-              const float s = __shfl_sync(~0u, inv, e);
+            for (int p0 = 0; p0 < P; p0 += PB) {
+              float4 h[R][PB];
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int p = 0; p < PB; ++p) {
+                  const int row = rank + splits * (w + 4 * min(j0 + r, nj - 1));   // (a row again where there are no more)
+                  const uint32_t from = smem_u32(part + (((p0 + p) & 1) * ROWS + row) * DP) + (((lane & (DP / 4 - 1)) ^ (row & 7)) << 4);
+                  h[r][p] = LP == 1 ? ld_shared_f4(from) : ld_cluster_f4(mapa_shared_at(from, (p0 + p) >> 1));
+                }
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int p = 0; p < PB; ++p) {
+                  const float fp = __shfl_sync(~0u, f, (min(j0 + r, nj - 1) << LP) + p0 + p);
+                  const bool any = fp != 0.f;   // a part without keys holds nothing
+                  o[r].x = fmaf(any ? h[r][p].x : 0.f, fp, o[r].x), o[r].y = fmaf(any ? h[r][p].y : 0.f, fp, o[r].y);
+                  o[r].z = fmaf(any ? h[r][p].z : 0.f, fp, o[r].z), o[r].w = fmaf(any ? h[r][p].w : 0.f, fp, o[r].w);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const int e = min(j0 + r, nj - 1) << LP;
+              const float q = __shfl_sync(~0u, inv, e);
               __nv_bfloat16* dst = a.out + __shfl_sync(~0u, at, e) + lane * 4;
-              if (lane * 4 < a.dim) {
+              const uint2 both = make_uint2(pack_bf16x2(o[r].x * q, o[r].y * q), pack_bf16x2(o[r].z * q, o[r].w * q));
+              if (j0 + r < nj && lane * 4 < a.dim) {
                 if (out_mode > 0) {
-                  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
+                  *reinterpret_cast<uint2*>(dst) = both;
                 } else {
-                  dst[0] = __float2bfloat16_rn(o.x * s), dst[1] = __float2bfloat16_rn(o.y * s);
-                  dst[2] = __float2bfloat16_rn(o.z * s), dst[3] = __float2bfloat16_rn(o.w * s);
+                  unsigned short* d = reinterpret_cast<unsigned short*>(dst);
+                  d[0] = (unsigned short)both.x, d[1] = (unsigned short)(both.x >> 16);
+                  d[2] = (unsigned short)both.y, d[3] = (unsigned short)(both.y >> 16);
                 }
               }
-              o = make_float4(0.f, 0.f, 0.f, 0.f);
             }
           }
-        }
+        };
+        if (lparts == 1) add_up(std::integral_constant<int, 1>());
+        else if (lparts == 2) add_up(std::integral_constant<int, 2>());
+        else if (lparts == 3) add_up(std::integral_constant<int, 3>());
+        else add_up(std::integral_constant<int, 4>());
         __syncwarp();
         if (lane < splits) mbar_arrive_cluster(mapa_shared(jempty, lane));
       }
@@ -791,38 +807,42 @@ inline CUtensorMap make_heads_tmap(const __nv_bfloat16* p, long long tokens, int
   return m;
 }
 
+// How a kernel would take a call: its time, roughly, in microseconds, the CTAs of a
+// cluster, and how many clusters there are.
+struct AttnPlan {
+  double time;
+  int splits, workers;
+};
+
+// Tiles of `pos` positions that the sequences can have at most.
+inline long long attn_tiles(const AttnArgs& a, int pos) { return std::min(a.total_q, a.total_q / pos + a.batch); }
+
+// The times are those of sequences all as long as the longest: rounds of tiles, a
+// time for each block of 128 keys and for a tile's first scores, output and join, and
+// for the launch.  Fitted to prompts of 64 to 4000 tokens and pieces of 16 to 300
+// queries over up to 8000 keys with 1 to 32 heads: the kernel chosen was the faster
+// one of each, or within 3 % of it.
 template <int DP, int ROWS>
-void launch_attention_as(const AttnArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                         int sms, int out_mode, cudaStream_t s) {
-  using Cfg = AttnCfg<DP, ROWS>;
-  auto kern = attention_kernel<DP, ROWS>;
-  allow_smem(kern, Cfg::SMEM, kAtRegs);
-  const long long units = a.max_tiles * a.kv_heads;
-  int splits = 1, workers = (int)std::min<long long>(units, sms);
-  if (ROWS > 0) {
-    // CTAs of a cluster: those that give the shortest time if all sequences are
-    // as long as the longest, with kAtJoinBlocks blocks' time lost on each tile
-    long long best = -1;
-    for (int n = 1; n <= 8; n *= 2) {
-      const int most = n > 1 ? max_clusters(kern, n, kAtThreads, Cfg::SMEM) : sms;
-      const long long time = (units + most - 1) / most * (((long long)a.max_k + n * kAtBN - 1) / (n * kAtBN) + kAtJoinBlocks);
-      if (best < 0 || time < best) best = time, splits = n, workers = (int)std::min<long long>(units, most);
-    }
+AttnPlan plan_attention(const AttnArgs& a, int sms) {
+  const int group = a.heads / a.kv_heads, pos = ROWS > 0 ? ROWS / group : 2 * (kAtBM / group);
+  const long long units = attn_tiles(a, pos) * a.kv_heads, blocks = ((long long)a.max_k + kAtBN - 1) / kAtBN;
+  if (ROWS == 0)
+    return {5 + 1.75 * (double)((units + sms - 1) / sms) * (double)(blocks + 1), 1, (int)std::min<long long>(units, sms)};
+  AttnPlan p = {-1, 1, 0};
+  for (int n = 1; n <= 8; n *= 2) {
+    const int most = n > 1 ? max_clusters(attention_kernel<DP, ROWS>, n, kAtThreads, AttnCfg<DP, ROWS>::SMEM) : sms;
+    const double time = 10 + (double)((units + most - 1) / most) * (0.9 * (double)((blocks + n - 1) / n) + 2);
+    if (p.time < 0 || time < p.time) p = {time, n, (int)std::min<long long>(units, most)};
   }
-  launch_op(s, splits, kern, dim3((unsigned)(workers * splits)), dim3(kAtThreads), Cfg::SMEM, mq, mk, mv, a, splits,
-            out_mode);
+  return p;
 }
 
-inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
-  const int group = a.heads / a.kv_heads;
-  // tiles of `pos` positions that the sequences can have at most
-  auto tiles = [&](int pos) { return std::min(a.total_q, a.total_q / pos + a.batch); };
-  // Positions of a 64-row tile are all there are, or too few 256-row tiles for the
-  // SMs: the halves, and the CTAs of a cluster, take parts of the keys instead.
-  const bool keys = group <= 64 && (a.max_q <= 64 / group || tiles(2 * (kAtBM / group)) * a.kv_heads * 2 <= sms);
-  const int rows = !keys ? 0 : group <= 16 && a.max_q <= 16 / group ? 16 : 64;
-  const int half_pos = (keys ? rows : kAtBM) / group;
-  a.max_tiles = tiles(keys ? half_pos : 2 * half_pos);
+template <int DP, int ROWS>
+void launch_attention_as(AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  using Cfg = AttnCfg<DP, ROWS>;
+  auto kern = attention_kernel<DP, ROWS>;
+  const int group = a.heads / a.kv_heads, half_pos = (ROWS > 0 ? ROWS : kAtBM) / group;
+  a.max_tiles = attn_tiles(a, ROWS > 0 ? half_pos : 2 * half_pos);
   const CUtensorMap mq = make_heads_tmap(a.q, a.total_q, a.heads, a.dim, a.q_t, a.q_h, half_pos, group);
   const bool none = a.total_k == 0;   // no key: the maps are not used, but they have to be valid
   const CUtensorMap mk = none ? mq : make_heads_tmap(a.k, a.total_k, a.kv_heads, a.dim, a.k_t, a.k_h, kAtBN, 1);
@@ -831,14 +851,28 @@ inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
     return (uintptr_t)a.out % bytes == 0 && a.o_t * 2 % bytes == 0 && a.o_h * 2 % bytes == 0;
   };
   const int out_mode = rows_aligned(32) ? 2 : rows_aligned(16) ? 1 : 0;
-  auto launch = [&](auto d) {
-    constexpr int DP = decltype(d)::value;
-    if (rows == 16) launch_attention_as<DP, 16>(a, mq, mk, mv, sms, out_mode, s);
-    else if (rows == 64) launch_attention_as<DP, 64>(a, mq, mk, mv, sms, out_mode, s);
-    else launch_attention_as<DP, 0>(a, mq, mk, mv, sms, out_mode, s);
-  };
-  if (a.dim > 64) launch(std::integral_constant<int, 128>());
-  else launch(std::integral_constant<int, 64>());
+  allow_smem(kern, Cfg::SMEM, kAtRegs);
+  launch_op(s, p.splits, kern, dim3((unsigned)(p.workers * p.splits)), dim3(kAtThreads), Cfg::SMEM, mq, mk, mv, a,
+            p.splits, out_mode);
+}
+
+template <int DP>
+void launch_attention_dim(AttnArgs& a, int sms, cudaStream_t s) {
+  const int group = a.heads / a.kv_heads;
+  const AttnPlan rows = plan_attention<DP, 0>(a, sms);
+  if (group <= 16 && a.max_q <= 16 / group) {
+    const AttnPlan keys = plan_attention<DP, 16>(a, sms);
+    if (keys.time < rows.time) return launch_attention_as<DP, 16>(a, keys, s);
+  } else if (group <= 64) {
+    const AttnPlan keys = plan_attention<DP, 64>(a, sms);
+    if (keys.time < rows.time) return launch_attention_as<DP, 64>(a, keys, s);
+  }
+  launch_attention_as<DP, 0>(a, rows, s);
+}
+
+inline void launch_attention(AttnArgs& a, int sms, cudaStream_t s) {
+  if (a.dim > 64) launch_attention_dim<128>(a, sms, s);
+  else launch_attention_dim<64>(a, sms, s);
 }
 
 }  // namespace gdit
