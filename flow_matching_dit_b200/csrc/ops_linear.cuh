@@ -6,8 +6,7 @@
 //                        epilogue of a tile runs under the products of the next
 //   linear_split_kernel  128 x BN tiles, K cut over the CTAs of a cluster, which
 //                        add their partial tiles through distributed shared
-//                        memory: few rows, few tiles, or an output that TMA
-//                        cannot address
+//                        memory: few rows or few tiles
 #pragma once
 
 #include <atomic>
@@ -27,6 +26,7 @@ struct LinearArgs {
   int n, k;
   int out_f32;
   int act;
+  int tma;   // pair kernel: TMA addresses out and residual
 };
 
 // Activations in f32.  v0 and v1 by 1 / (1 + 2^-a) of theirs, with one reciprocal for
@@ -94,6 +94,55 @@ __device__ __forceinline__ void lin_pair_tile(int t, int mt, int nt, int& mi, in
   const int gs = 8 * nt, g = t / gs, first = g * 8, gm = min(mt - first, 8), r = t - g * gs;
   mi = first + r % gm;
   ni = r / gm;
+}
+
+// A warp's box of 32 rows x 128 bytes (128-byte swizzle), from and to a matrix that TMA
+// cannot address: rows from `row`, columns from n, a word a lane.  Reads behind the
+// matrix' edges are moved onto it (what they give is not stored): a branch around each
+// of them costs more than the reads.
+__device__ __forceinline__ uint32_t* box_word(uint8_t* box, int r) {
+  const int lane = threadIdx.x & 31;
+  return reinterpret_cast<uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+}
+
+__device__ __forceinline__ void box_from(uint8_t* box, const void* p, long long ld, int f32, long long row, long long m,
+                                         int n, int cols) {
+  const int lane = threadIdx.x & 31, c = n + (f32 ? lane : 2 * lane);
+  const int c0 = min(c, cols - 1), c1 = min(c + 1, cols - 1);
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 16) {
+    uint32_t v[16];
+    if (f32) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = static_cast<const uint32_t*>(p)[min(row + r0 + r, m - 1) * ld + c0];
+    } else {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const unsigned short* q = static_cast<const unsigned short*>(p) + min(row + r0 + r, m - 1) * ld;
+        v[r] = q[c0] | (uint32_t)q[c1] << 16;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) *box_word(box, r0 + r) = v[r];
+  }
+}
+
+__device__ __forceinline__ void box_to(uint8_t* box, void* p, long long ld, int f32, long long row, long long m, int n,
+                                       int cols) {
+  const int lane = threadIdx.x & 31, c = n + (f32 ? lane : 2 * lane);
+  const int rows = (int)min((long long)32, m - row);
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    const uint32_t v = *box_word(box, r);
+    const long long at = (row + r) * ld + c;
+    if (f32) {
+      if (r < rows && c < cols) static_cast<uint32_t*>(p)[at] = v;
+    } else {
+      unsigned short* q = static_cast<unsigned short*>(p) + at;
+      if (r < rows && c < cols) q[0] = (unsigned short)v;
+      if (r < rows && c + 1 < cols) q[1] = (unsigned short)(v >> 16);
+    }
+  }
 }
 
 template <int BN>
@@ -204,7 +253,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint64_t* rbar = rfull + 2 * ew;
     const int cols = a.out_f32 ? 32 : 64, chunks = BN / cols / 2;   // columns of a box, boxes of this warp in a tile
     const int sw = lane & 7;
-    const bool res = a.residual != nullptr;
+    const bool res = a.residual != nullptr, res_tma = res && a.tma;
     int it = 0, seq = 0;
     for (int t = cid; t < total; t += ncl, ++it) {
       lin_pair_tile(t, mt, nt, mi, ni);
@@ -216,7 +265,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tma_load_2d(boxes + (s & 1) * 4096, &tmR, &rbar[s & 1], n, ym);
         }
       };
-      if (res) fetch(seq, n0);
+      auto gather = [&](int s, int n) {   // residual box of chunk s, without TMA
+        box_from(boxes + (s & 1) * 4096, a.residual, a.ldr, a.out_f32, ym, a.m, n, a.n);
+      };
+      if (res_tma) {
+        fetch(seq, n0);
+      } else if (res && ym < a.m) {
+        for (int c = 0; c < min(2, chunks); ++c) gather(seq + c, n0 + c * 2 * cols);
+      }
       op_wait_through(&tfull[buf], (it >> 1) & 1, &s_abort);
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + half * cols;
@@ -233,7 +289,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty_l + 8u * buf);
         }
-        if (res) {
+        if (!a.tma) {
+          __syncwarp();
+        } else if (res) {
           op_wait_through(&rbar[seq & 1], (seq >> 1) & 1, &s_abort);
           if (c + 1 < chunks) fetch(seq + 1, n + 2 * cols);
           __syncwarp();
@@ -285,6 +343,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             *p = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
                             pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
           }
+        }
+        if (!a.tma) {
+          __syncwarp();
+          if (ym < a.m) box_to(box, a.out, a.ldo, a.out_f32, ym, a.m, n, a.n);
+          __syncwarp();
+          if (res && ym < a.m && c + 2 < chunks) gather(seq + 2, n + 4 * cols);
+          continue;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -536,8 +601,9 @@ template <int BN>
 void launch_linear_pair(const LinearArgs& a, int sms, cudaStream_t s) {
   using Cfg = LinPairCfg<BN>;
   const CUtensorMap tx = make_tmap(a.x, a.m, a.k, a.ldx, 128), tw = make_tmap(a.w, a.n, a.k, a.ldw, BN / 2);
-  const CUtensorMap to = make_box_tmap(a.out, a.out_f32, a.m, a.n, a.ldo);
-  const CUtensorMap tr = a.residual != nullptr ? make_box_tmap(a.residual, a.out_f32, a.m, a.n, a.ldr) : to;
+  // (without TMA for the output the maps are not used, but they have to be valid)
+  const CUtensorMap to = a.tma ? make_box_tmap(a.out, a.out_f32, a.m, a.n, a.ldo) : tx;
+  const CUtensorMap tr = a.tma && a.residual != nullptr ? make_box_tmap(a.residual, a.out_f32, a.m, a.n, a.ldr) : to;
   const long long tiles = (a.m + 255) / 256 * ((a.n + BN - 1) / BN);
   REQUIRE(tiles <= INT32_MAX / 2, "m %lld x n %d has too many tiles", a.m, a.n);
   allow_smem(linear_pair_kernel<BN>, Cfg::SMEM);
@@ -608,12 +674,12 @@ inline SplitPlan plan_split(long long m, int n, int k, int sms) {
   return p;
 }
 
-inline void launch_linear(const LinearArgs& a, int sms, cudaStream_t s) {
+inline void launch_linear(LinearArgs& a, int sms, cudaStream_t s) {
   const int es = a.out_f32 ? 4 : 2;
   auto tma_ok = [&](const void* p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld * es % 16 == 0; };
-  const bool tma = tma_ok(a.out, a.ldo) && (a.residual == nullptr || tma_ok(a.residual, a.ldr));
+  a.tma = tma_ok(a.out, a.ldo) && (a.residual == nullptr || tma_ok(a.residual, a.ldr));
   const long long mt = (a.m + 255) / 256;
-  if (tma && mt * ((a.n + 127) / 128) >= sms / 2) {
+  if (mt * ((a.n + 127) / 128) >= sms / 2) {
     // Rounds of tiles over the pairs times the time of a step of 64 along K, which is
     // what a CTA loads for it (at about 51 bytes a cycle from L2) or the product:
     // 32 KB and 512 cycles at 256 columns, 24 KB and 256 cycles at 128

@@ -169,6 +169,29 @@ def test_linear_split_plans(m, n, k):
     check_linear(m, n, k, "none", "f32", False, True)
 
 
+@pytest.mark.parametrize("m, n, k", [(2500, 2051, 136), (1821, 6388, 24), (4099, 1030, 520), (1111, 4097, 64)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_many_rows_that_no_box_fits(m, n, k, out):
+    """Outputs and residuals whose rows begin anywhere, over many tiles; and slices with room that stays as it was."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    check_linear(m, n, k, "gelu", out, True, True)
+    check_linear(m, n, k, "none", out, False, False)
+    g = gen(n)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    x, w = rnd(g, m, k, dtype=torch.bfloat16), rnd(g, n, k, std=k ** -0.5, dtype=torch.bfloat16)
+    wide = torch.full((m, n + 6), 5.0, device="cuda", dtype=dt)
+    r = rnd(g, m, n + 1, dtype=dt)[:, 1:]
+    out_ = wide[:, 3:3 + n]
+    linear(x, w, residual=r, out=out_)
+    within(out_, *linear64(x, w, None, "none", r, dt))
+    assert (wide[:, :3] == 5).all() and (wide[:, 3 + n:] == 5).all()
+    out_.copy_(r)
+    linear(x, w, residual=out_, out=out_)   # in place
+    within(out_, *linear64(x, w, None, "none", r, dt))
+    clean()
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("m", [4, 1100])
 def test_linear_activations_far_out(act, m):
