@@ -385,12 +385,13 @@ constexpr int kSplitThreads = 256;
 constexpr int kSplitSmem = 226 * 1024;   // at most: the kernel has some bytes of its own
 
 struct SplitPlan {
+  double time;   // microseconds
   int bn, splits, stages, xrows;
   int smem() const { return 1024 + std::max(stages * (xrows + bn) * 128 + (128 - xrows) * 128, 128 * bn * 4) + 512; }
 };
 
 template <int BN>
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(kSplitThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                         const LinearArgs a, int splits, int stages, int xrows, int smem_bytes) {
   extern __shared__ uint8_t smem_raw[];
@@ -503,44 +504,53 @@ __global__ void __launch_bounds__(kSplitThreads)
     const int col = (lane % LANES) * 4, n = n0 + col, left = a.n - n;   // columns from here on
     const int stride = 8 * PER * splits;
     const int es = a.out_f32 ? 4 : 2;
-    const bool vec = left >= 4 && ((uintptr_t)a.out % (4 * es) == 0) && a.ldo % 4 == 0 &&
+    // by fours: the tile's columns are all there, rows begin at multiples of four
+    const bool vec = n0 + BN <= a.n && ((uintptr_t)a.out % (4 * es) == 0) && a.ldo % 4 == 0 &&
                      (a.residual == nullptr || ((uintptr_t)a.residual % (4 * es) == 0 && a.ldr % 4 == 0));
+    int at_col[4];   // (columns behind the last are read as the last and not written: no branches around the reads)
     float bias[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bias[e] = a.bias != nullptr && e < left ? __ldg(a.bias + n + e) : 0.f;
-    uint32_t base[8];
+    for (int e = 0; e < 4; ++e) at_col[e] = min(n + e, a.n - 1);
 #pragma unroll
-    for (int s = 0; s < 8; ++s) base[s] = s < splits ? (splits > 1 ? mapa_shared(part, s) : smem_u32(part)) : 0;
+    for (int e = 0; e < 4; ++e) bias[e] = a.bias != nullptr ? __ldg(a.bias + at_col[e]) : 0.f;
     for (int r0 = rank + splits * (warp * PER + lane / LANES); r0 < rows; r0 += 4 * stride) {
       float v[4][4], res[4][4];
+      if (a.residual != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + i * stride;
-        if (row >= rows || left <= 0) continue;
-        if (a.residual != nullptr) {
-          const long long at = (m0 + row) * a.ldr + n;
+        for (int i = 0; i < 4; ++i) {
+          if (splits > 1 && r0 + i * stride >= rows) continue;
+          const long long row = (m0 + min(r0 + i * stride, rows - 1)) * a.ldr;
           if (a.out_f32) {
-            const float* p = static_cast<const float*>(a.residual) + at;
-            if (vec) *reinterpret_cast<float4*>(res[i]) = *reinterpret_cast<const float4*>(p);
-            else
+            const float* p = static_cast<const float*>(a.residual) + row;
+            if (vec) {
+              *reinterpret_cast<float4*>(res[i]) = *reinterpret_cast<const float4*>(p + n);
+            } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) res[i][e] = e < left ? p[e] : 0.f;
+              for (int e = 0; e < 4; ++e) res[i][e] = p[at_col[e]];
+            }
           } else {
-            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.residual) + at;
-            if (vec) *reinterpret_cast<float4*>(res[i]) = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p));
-            else
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.residual) + row;
+            if (vec) {
+              *reinterpret_cast<float4*>(res[i]) = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + n));
+            } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) res[i][e] = e < left ? __bfloat162float(p[e]) : 0.f;
+              for (int e = 0; e < 4; ++e) res[i][e] = __bfloat162float(p[at_col[e]]);
+            }
           }
         }
-        const uint32_t at = (uint32_t)(row * BN + ((((col >> 2) ^ (row & 7))) << 2)) * 4u;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (splits > 1 && r0 + i * stride >= rows) continue;   // (reads through the cluster are the dear ones)
+        const int row = min(r0 + i * stride, rows - 1);
+        const uint32_t at = smem_u32(part) + (uint32_t)(row * BN + (((col >> 2) ^ (row & 7)) << 2)) * 4u;
         if (splits == 1) {
-          *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(part) + at);
+          *reinterpret_cast<float4*>(v[i]) = ld_shared_f4(at);
         } else {
           float4 f[8];
 #pragma unroll
           for (int s = 0; s < 8; ++s)
-            if (s < splits) f[s] = ld_cluster_f4(base[s] + at);
+            if (s < splits) f[s] = ld_cluster_f4(mapa_shared_at(at, s));
           *reinterpret_cast<float4*>(v[i]) = f[0];
 #pragma unroll
           for (int s = 1; s < 8; ++s)
@@ -549,8 +559,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = r0 + i * stride;
-        if (row >= rows || left <= 0) continue;
+        if (splits > 1 && r0 + i * stride >= rows) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[i][e] += bias[e];
         apply_act(a.act, v[i]);
@@ -558,21 +567,27 @@ __global__ void __launch_bounds__(kSplitThreads)
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[i][e] += res[i][e];
         }
+        const int row = r0 + i * stride;
         const long long at = (m0 + row) * a.ldo + n;
         if (a.out_f32) {
           float* p = static_cast<float*>(a.out) + at;
-          if (vec) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(v[i]);
-          else
+          if (vec) {
+            if (row < rows) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(v[i]);
+          } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (e < left) p[e] = v[i][e];
+              if (row < rows && e < left) p[e] = v[i][e];
+          }
         } else {
           __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
-          if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
-          else
+          if (vec) {
+            if (row < rows)
+              *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
+          } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (e < left) p[e] = __float2bfloat16_rn(v[i][e]);
+              if (row < rows && e < left) p[e] = __float2bfloat16_rn(v[i][e]);
+          }
         }
       }
     }
@@ -644,6 +659,10 @@ inline const SplitSlots& split_slots(int sms) {
   return *p;
 }
 
+// Which kernel, tile width and parts of K: those with the shortest time by this and
+// pair_time.  The coefficients fit the times of 80 sizes (1 to 16384 rows, 16 to 8192
+// columns, K of 32 to 8192, aligned and odd) in up to 23 plans each; the plan chosen took
+// 3 % longer than the best one on average, 24 % at most.
 inline SplitPlan plan_split(long long m, int n, int k, int sms) {
   SplitPlan p = {};
   const SplitSlots& slots = split_slots(sms);
@@ -651,21 +670,16 @@ inline SplitPlan plan_split(long long m, int n, int k, int sms) {
   const long long mt = (m + 127) / 128;
   p.xrows = 8;
   while (p.xrows < 128 && p.xrows < m) p.xrows *= 2;
-  // The tile width and the parts of K with the shortest time, in microseconds: a CTA's
-  // own (its start, its steps along K, the kilobytes it loads, its share of the tile's
-  // rows to write), times the CTAs for each place, and the join.  The coefficients fit
-  // the times of 78 sizes (1 to 2048 rows, 16 to 8192 columns, K of 32 to 8192) in up to
-  // 21 plans each; the plan chosen took 4 % longer than the best one on average, 31 % at
-  // most.
-  double best = 0;
+  // A CTA's own time (its start, its steps along K, the kilobytes it loads, its share of
+  // the tile's rows to write), times the CTAs for each place, and the join.
   const int rows = (int)std::min<long long>(m, 128);
   for (int bn = 128; bn >= 32; bn /= 2)
     for (int s = 1; s <= 8 && (s == 1 || 2 * s <= nkb); ++s) {
       const int steps = (nkb + s - 1) / s;
-      const double own = 1.18 + 0.116 * steps + 0.0069 * steps * (p.xrows + bn) / 8 + 5.35 * rows * bn / 16384 / s;
+      const double own = 1.63 + 0.120 * steps + 0.0063 * steps * (p.xrows + bn) / 8 + 4.6 * rows * bn / 16384 / s;
       const double places = (double)(mt * ((n + bn - 1) / bn) * s) / slots.of[s];
-      const double time = own * std::max(1.0, places) + (s > 1 ? 1.2 + 0.04 * s : 0);
-      if (p.bn == 0 || time < best) best = time, p.bn = bn, p.splits = s;
+      const double time = own * std::max(1.0, places) + (s > 1 ? 0.89 + 0.096 * s : 0);
+      if (p.bn == 0 || time < p.time) p.time = time, p.bn = bn, p.splits = s;
     }
   const long long ctas = mt * ((n + p.bn - 1) / p.bn) * p.splits;
   const int per = (nkb + p.splits - 1) / p.splits;
@@ -674,22 +688,26 @@ inline SplitPlan plan_split(long long m, int n, int k, int sms) {
   return p;
 }
 
+// The pair kernel's time in microseconds: rounds of tiles over the pairs, a step along K
+// at what its loads take, and an epilogue that runs under the next tile's products.
+inline double pair_time(const LinearArgs& a, int bn, int sms) {
+  const long long tiles = (a.m + 255) / 256 * ((a.n + bn - 1) / bn), pairs = sms / 2;
+  const double rounds = (double)((tiles + pairs - 1) / pairs), products = (a.k + 63) / 64 * 0.33 * (128 + bn / 2) / 256;
+  const double epilogue = (a.tma ? 6.8 : 9.8) * bn / 256;
+  return 1.2 + std::max(rounds * products + epilogue, rounds * std::max(products, epilogue));
+}
+
 inline void launch_linear(LinearArgs& a, int sms, cudaStream_t s) {
   const int es = a.out_f32 ? 4 : 2;
   auto tma_ok = [&](const void* p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld * es % 16 == 0; };
   a.tma = tma_ok(a.out, a.ldo) && (a.residual == nullptr || tma_ok(a.residual, a.ldr));
-  const long long mt = (a.m + 255) / 256;
-  if (mt * ((a.n + 127) / 128) >= sms / 2) {
-    // Rounds of tiles over the pairs times the time of a step of 64 along K, which is
-    // what a CTA loads for it (at about 51 bytes a cycle from L2) or the product:
-    // 32 KB and 512 cycles at 256 columns, 24 KB and 256 cycles at 128
-    const long long pairs = sms / 2, wide = (mt * ((a.n + 255) / 256) + pairs - 1) / pairs * 640,
-                    narrow = (mt * ((a.n + 127) / 128) + pairs - 1) / pairs * 480;
-    if (wide <= narrow) launch_linear_pair<256>(a, sms, s);
+  const SplitPlan p = plan_split(a.m, a.n, a.k, sms);
+  const double wide = pair_time(a, 256, sms), narrow = pair_time(a, 128, sms);
+  if (std::min(wide, narrow) < p.time) {
+    if (wide < narrow) launch_linear_pair<256>(a, sms, s);
     else launch_linear_pair<128>(a, sms, s);
     return;
   }
-  const SplitPlan p = plan_split(a.m, a.n, a.k, sms);
   if (p.bn == 128) launch_linear_split<128>(a, p, s);
   else if (p.bn == 64) launch_linear_split<64>(a, p, s);
   else launch_linear_split<32>(a, p, s);
