@@ -10,6 +10,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "gemm_tc.cuh"
 #include "ops_common.cuh"
@@ -498,8 +499,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
   if (splits > 1) cluster_sync();
   if (ok) {
-    // lane: 4 columns of a row, BN / 4 lanes a row; its rows are `stride` apart.
-    // Four of them at a time, so that their reads are under way together.
+    // lane: 4 columns of a row, BN / 4 lanes a row; its rows are `stride` apart
     constexpr int LANES = BN / 4, PER = 32 / LANES;
     const int col = (lane % LANES) * 4, n = n0 + col, left = a.n - n;   // columns from here on
     const int stride = 8 * PER * splits;
@@ -513,84 +513,89 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     for (int e = 0; e < 4; ++e) at_col[e] = min(n + e, a.n - 1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) bias[e] = a.bias != nullptr ? __ldg(a.bias + at_col[e]) : 0.f;
-    for (int r0 = rank + splits * (warp * PER + lane / LANES); r0 < rows; r0 += 4 * stride) {
-      float v[4][4], res[4][4];
-      if (a.residual != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (splits > 1 && r0 + i * stride >= rows) continue;
-          const long long row = (m0 + min(r0 + i * stride, rows - 1)) * a.ldr;
-          if (a.out_f32) {
-            const float* p = static_cast<const float*>(a.residual) + row;
-            if (vec) {
-              *reinterpret_cast<float4*>(res[i]) = *reinterpret_cast<const float4*>(p + n);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) res[i][e] = p[at_col[e]];
-            }
-          } else {
-            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.residual) + row;
-            if (vec) {
-              *reinterpret_cast<float4*>(res[i]) = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + n));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) res[i][e] = __bfloat162float(p[at_col[e]]);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (splits > 1 && r0 + i * stride >= rows) continue;   // (reads through the cluster are the dear ones)
-        const int row = min(r0 + i * stride, rows - 1);
-        const uint32_t at = smem_u32(part) + (uint32_t)(row * BN + (((col >> 2) ^ (row & 7)) << 2)) * 4u;
-        if (splits == 1) {
-          *reinterpret_cast<float4*>(v[i]) = ld_shared_f4(at);
-        } else {
-          float4 f[8];
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            if (s < splits) f[s] = ld_cluster_f4(mapa_shared_at(at, s));
-          *reinterpret_cast<float4*>(v[i]) = f[0];
-#pragma unroll
-          for (int s = 1; s < 8; ++s)
-            if (s < splits) v[i][0] += f[s].x, v[i][1] += f[s].y, v[i][2] += f[s].z, v[i][3] += f[s].w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (splits > 1 && r0 + i * stride >= rows) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[i][e] += bias[e];
-        apply_act(a.act, v[i]);
+    // R rows at a time: four of a whole tile, so that their reads are under way together; one where the CTAs of a
+    // cluster share few rows, since four times the instructions would have to be fetched
+    auto write_rows = [&](auto count) {
+      constexpr int R = decltype(count)::value;
+#pragma unroll 1
+      for (int r0 = rank + splits * (warp * PER + lane / LANES); r0 < rows; r0 += R * stride) {
+        float v[R][4], res[R][4];
         if (a.residual != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[i][e] += res[i][e];
-        }
-        const int row = r0 + i * stride;
-        const long long at = (m0 + row) * a.ldo + n;
-        if (a.out_f32) {
-          float* p = static_cast<float*>(a.out) + at;
-          if (vec) {
-            if (row < rows) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(v[i]);
-          } else {
+          for (int i = 0; i < R; ++i) {
+            const long long row = (m0 + min(r0 + i * stride, rows - 1)) * a.ldr;
+            if (a.out_f32) {
+              const float* p = static_cast<const float*>(a.residual) + row;
+              if (vec) {
+                *reinterpret_cast<float4*>(res[i]) = *reinterpret_cast<const float4*>(p + n);
+              } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (row < rows && e < left) p[e] = v[i][e];
+                for (int e = 0; e < 4; ++e) res[i][e] = p[at_col[e]];
+              }
+            } else {
+              const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.residual) + row;
+              if (vec) {
+                *reinterpret_cast<float4*>(res[i]) = bf16x4_to_f32(*reinterpret_cast<const uint2*>(p + n));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) res[i][e] = __bfloat162float(p[at_col[e]]);
+              }
+            }
           }
-        } else {
-          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
-          if (vec) {
-            if (row < rows)
-              *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
-          } else {
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (row < rows && e < left) p[e] = __float2bfloat16_rn(v[i][e]);
+        for (int i = 0; i < R; ++i) {
+          const int row = min(r0 + i * stride, rows - 1);
+          const uint32_t at = smem_u32(part) + (uint32_t)(row * BN + (((col >> 2) ^ (row & 7)) << 2)) * 4u;
+          if (R > 1) {
+            *reinterpret_cast<float4*>(v[i]) = ld_shared_f4(at);
+          } else {
+            float4 f[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              if (s < splits) f[s] = ld_cluster_f4(mapa_shared_at(at, s));
+            *reinterpret_cast<float4*>(v[i]) = f[0];
+#pragma unroll
+            for (int s = 1; s < 8; ++s)
+              if (s < splits) v[i][0] += f[s].x, v[i][1] += f[s].y, v[i][2] += f[s].z, v[i][3] += f[s].w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][e] += bias[e];
+          apply_act(a.act, v[i]);
+          if (a.residual != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] += res[i][e];
+          }
+          const int row = r0 + i * stride;
+          const long long at = (m0 + row) * a.ldo + n;
+          if (a.out_f32) {
+            float* p = static_cast<float*>(a.out) + at;
+            if (vec) {
+              if (row < rows) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(v[i]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (row < rows && e < left) p[e] = v[i][e];
+            }
+          } else {
+            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
+            if (vec) {
+              if (row < rows)
+                *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (row < rows && e < left) p[e] = __float2bfloat16_rn(v[i][e]);
+            }
           }
         }
       }
-    }
+    };
+    if (splits == 1) write_rows(std::integral_constant<int, 4>());
+    else write_rows(std::integral_constant<int, 1>());
   }
   if (splits > 1) cluster_sync();   // nobody leaves while its partial tile is read
 }
