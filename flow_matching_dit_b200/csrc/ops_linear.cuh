@@ -7,6 +7,10 @@
 //   linear_split_kernel  128 x BN tiles, K cut over the CTAs of a cluster, which
 //                        add their partial tiles through distributed shared
 //                        memory: few rows or few tiles
+// 16384 x 8192 x 2048 with GELU: 437 us, 1.26 PFLOP/s of 1.63 measured (of 1.38
+// under the power limit, which holds this size to 1.6 GHz).  Middle sizes are bound by
+// what the SMs load from L2, about 51 bytes a cycle each, and the epilogue of their one
+// or two tiles (1237 x 2056 x 1096: 17 us); one token by latency (4.3 us).
 #pragma once
 
 #include <atomic>

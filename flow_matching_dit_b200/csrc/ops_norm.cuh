@@ -24,8 +24,11 @@ struct NormArgs {
 };
 
 // A row is held in registers by a team of whole warps, 4 * NU values a thread,
-// and read and written once; two rows of a warp are never in flight, other warps
-// hide its latency.  What bounds it: memory (h and y in, h' and u out).
+// and read and written once; a team takes one row at a time, other teams hide its
+// latency.  What bounds it: memory (h and y in, h' and u out): 65536 x 2048 in
+// 276 us, 5.8 TB/s of the 6.46 that a copy reaches.  Few rows are bound by the
+// latency of one (17 x 1024: 3.3 us), odd widths by the vectors of the channels,
+// which are then read value by value (2999 x 1337: 19 us, 1.7 TB/s).
 // A warp of the team takes 128 * NU neighbouring values, so that a thread's
 // addresses differ by constants:
 //   kUnits    lane i holds the 4-value units i, i + 32, ...: 16 bytes of f32 or 8 of bf16

@@ -371,6 +371,8 @@ int gdit_gemm_static_scratch(const void* A, const void* B, const float* bias, fl
  *     max_q / max_k.  Nothing is read or written outside the tensors for them;
  *     the call's affected rows are NaN (row_group) or left as they were
  *     (attention), and gdit_op_status reports GDIT_EDEVICE.
+ *   - Waits inside the kernels are bounded (2 s).  After one has run out the
+ *     call ends, what it wrote is void, and gdit_op_status reports GDIT_ETIMEOUT.
  *   - Every call returns GDIT_OK, GDIT_EINVAL, GDIT_ECUDA or GDIT_ENODEV; the
  *     detail message is gdit_last_error(NULL) on the same thread. */
 

@@ -890,6 +890,37 @@ def test_binding_refusals():
     clean()
 
 
+def test_first_calls_of_a_process_inside_a_capture():
+    """No set-up call is needed: every kernel's first call may be a captured one."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from flow_matching_dit_b200 import attention, linear, norm_residual, op_status
+bf = torch.bfloat16
+g = torch.Generator(device="cuda").manual_seed(0)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+x, w, wide = r(3, 1024).to(bf), r(512, 1024).to(bf), r(2048, 1024).to(bf)
+h, y = r(40, 513), r(40, 513).to(bf)
+q, kv, cq, ck = r(2, 8, 128).to(bf), r(6000, 2, 128).to(bf), torch.tensor([0, 1, 2]), torch.tensor([0, 3000, 6000])
+p, cp = r(500, 8, 64).to(bf), torch.tensor([0, 200, 500])
+cq, ck, cp = (t.int().cuda() for t in (cq, ck, cp))
+def calls():
+    return [linear(x, w), linear(wide, wide, activation="gelu"), *norm_residual(h, y, post="rms", pre="layer"),
+            attention(q, kv, kv, cq, ck, max_q=1, max_k=3000), attention(p, p[:, :4], p[:, 4:], cp, cp, max_q=300, max_k=300)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, calls())) and op_status() == 0
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 def test_on_a_stream_of_its_own_and_by_handle():
     import torch
     from flow_matching_dit_b200 import linear, op_status
