@@ -220,26 +220,31 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// mode 2: rows aligned to 32 bytes, 1: to 16 bytes, 0: to their elements
-__device__ __forceinline__ void store_out_row(__nv_bfloat16* o, int mode, int c0, int dim, const float (&v)[32]) {
-  uint32_t w[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-  if (mode == 2 && c0 + 32 <= dim) {
+// The first `cols` of 32 bf16 of a row, where ok.  mode 2: rows aligned to 32 bytes, 1:
+// to 16 bytes, 0: to their elements.  Predicated, without branches on ok.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* o, int mode, int cols, const uint32_t (&w)[16], bool ok) {
+  if (mode == 2 && cols == 32) {
 #pragma unroll
     for (int j = 0; j < 16; j += 8)
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + c0 + 2 * j), "r"(w[j]),
-                   "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]), "r"(w[j + 6]), "r"(w[j + 7])
-                   : "memory");
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %9, 0;\n\t"
+          "@p st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t}" ::"l"(o + 2 * j),
+          "r"(w[j]), "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]), "r"(w[j + 6]),
+          "r"(w[j + 7]), "r"((int)ok)
+          : "memory");
   } else if (mode >= 1) {
 #pragma unroll
     for (int j = 0; j < 16; j += 4)
-      if (c0 + 2 * j < dim)
-        *reinterpret_cast<uint4*>(o + c0 + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+          "@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(o + 2 * j),
+          "r"(w[j]), "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"((int)(ok && 2 * j < cols))
+          : "memory");
   } else {
+    unsigned short* q = reinterpret_cast<unsigned short*>(o);
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (c0 + j < dim) o[c0 + j] = __float2bfloat16_rn(v[j]);
+      if (ok && j < cols) q[j] = (unsigned short)(w[j >> 1] >> (16 * (j & 1)));
   }
 }
 
@@ -740,16 +745,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int head = t.kvh * group + row_head;
         __nv_bfloat16* orow = a.out + (t.s.q0 + pos) * a.o_t + head * a.o_h;
         if (active) {
+          const bool nothing = sum == 0.f;   // (what TMEM holds of a row without keys does not matter)
 #pragma unroll 1
           for (int x = 0; x < a.dim; x += 32) {
-            float v[32] = {};
-            if (done > 0) {
-              tmem_ld32(tO + x, reinterpret_cast<uint32_t(&)[32]>(v));
-              tmem_ld_wait();
-            }
+            float v[32];
+            tmem_ld32(tO + x, reinterpret_cast<uint32_t(&)[32]>(v));
+            tmem_ld_wait();
+            uint32_t w[16];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = sum == 0.f ? 0.f : v[y] * inv;
-            if (valid) store_out_row(orow, out_mode, x, a.dim, v);
+            for (int y = 0; y < 16; ++y) {
+              const uint32_t both = pack_bf16x2(v[2 * y] * inv, v[2 * y + 1] * inv);
+              w[y] = nothing ? 0u : both;
+            }
+            store_row32(orow + x, out_mode, min(32, a.dim - x), w, valid);
           }
         }
         if (valid && a.lse != nullptr)
