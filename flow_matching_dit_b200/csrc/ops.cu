@@ -58,7 +58,8 @@ bool aligned_to(const void* p, int bytes) { return ((uintptr_t)p % (uintptr_t)by
 
 // Strides times sizes stay far inside 64 bits.
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
-constexpr int64_t kMaxRows = (int64_t)INT32_MAX;
+// Rows, columns and keys: the last tile's end still fits 32 bits.
+constexpr int64_t kMaxRows = (int64_t)INT32_MAX - 1024;
 
 __global__ void clear_status_kernel(unsigned bits) { atomicAnd(&g_op_status, ~bits); }
 
@@ -71,6 +72,7 @@ int gdit_linear(const gdit_linear_args* p, void* cuda_stream) {
     REQUIRE(p != nullptr, "NULL arguments");
     REQUIRE(p->m >= 0 && p->m <= kMaxRows, "m %lld out of range", (long long)p->m);
     REQUIRE(p->n >= 1 && p->k >= 8 && p->k % 8 == 0, "need n >= 1 and k >= 8, a multiple of 8 (n %d, k %d)", p->n, p->k);
+    REQUIRE(p->n <= kMaxRows && p->k <= kMaxRows, "n %d or k %d out of range", p->n, p->k);
     REQUIRE(is_dtype(p->out_dtype), "out_dtype %d", p->out_dtype);
     REQUIRE(p->activation >= GDIT_ACT_NONE && p->activation <= GDIT_ACT_SILU, "activation %d", p->activation);
     if (p->m == 0) return;

@@ -195,7 +195,7 @@ struct TileWalk {
     t.p0 = level * tile_pos;
     t.np = min(tile_pos, t.s.nq - t.p0);
     t.end = t.s.nk;
-    if (a.causal) t.end = max(0, min(t.s.nk, t.p0 + t.np + t.s.nk - t.s.nq));
+    if (a.causal) t.end = max(0, min(t.s.nk, t.p0 + t.np + (t.s.nk - t.s.nq)));
     const int blocks = (t.end + kAtBN - 1) / kAtBN;
     t.b0 = KEYS ? (int)((long long)rank * blocks / splits) : 0;
     t.nb = KEYS ? (int)((long long)(rank + 1) * blocks / splits) - t.b0 : blocks;
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const bool valid = row_pos < half_pos && first_pos + row_pos < t.np;
       const bool active = __any_sync(~0u, valid);      // a warp without rows only keeps the tensor core going
       int limit = valid ? t.s.nk : 0;                  // keys that this row sees
-      if (a.causal && valid) limit = max(0, min(limit, pos + t.s.nk - t.s.nq + 1));
+      if (a.causal && valid) limit = max(0, min(limit, pos + (t.s.nk - t.s.nq) + 1));
       float top = -INFINITY, sum = 0.f;
       int done = 0;                                    // blocks of this half
       // ROWS = 16: a quad of lanes has the rows quad and quad + 8, two neighbouring keys of every eight a lane; in the

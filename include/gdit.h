@@ -395,9 +395,9 @@ int gdit_gemm_static_scratch(const void* A, const void* B, const float* bias, fl
  *   residual  out_dtype [m, n], row stride ldr, or NULL; may be out itself
  *   out       out_dtype (GDIT_F32 or GDIT_BF16) [m, n], row stride ldo; must
  *             not overlap x or w
- * m >= 0; n >= 1; k >= 8, a multiple of 8; x and w 16-byte aligned, ldx and
- * ldw multiples of 8 and >= k; ldr and ldo >= n; bias, residual and out
- * aligned to their element. */
+ * m >= 0; n >= 1; k >= 8, a multiple of 8; m, n and k up to
+ * 2^31 - 1025; x and w 16-byte aligned, ldx and ldw multiples of 8 and >= k;
+ * ldr and ldo >= n; bias, residual and out aligned to their element. */
 typedef struct {
   const void* x;
   const void* w;
@@ -474,7 +474,8 @@ int gdit_norm_residual(const gdit_norm_args* a, void* cuda_stream);
  * reaches also the queries of which it is hidden.
  * heads a multiple of kv_heads; heads / kv_heads <= 128; head_dim a multiple
  * of 8 in [8, 128]; q, k, v 16-byte aligned with strides that are multiples of
- * 8; total_k and total_q heads / kv_heads below 2^31 - 256; batch in [0, 65535]; scale finite. */
+ * 8; total_k and total_q * heads / kv_heads up to 2^31 - 1281; batch in
+ * [0, 65535]; scale finite. */
 typedef struct {
   const void* q;
   const void* k;

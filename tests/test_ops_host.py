@@ -60,7 +60,9 @@ def linear_args(**over):
 
 @pytest.mark.parametrize("over, word", [
     (dict(x=None), "NULL"), (dict(w=None), "NULL"), (dict(out=None), "NULL"), (dict(m=-1), "m -1"),
-    (dict(m=1 << 31), "out of range"), (dict(n=0), "n >= 1"), (dict(k=0), "k >= 8"), (dict(k=60), "multiple of 8"),
+    (dict(m=1 << 31), "out of range"), (dict(m=2 ** 31 - 1024), "out of range"),
+    (dict(n=2 ** 31 - 1, ldo=1 << 32), "out of range"), (dict(k=2 ** 31 - 8, ldx=1 << 32, ldw=1 << 32), "out of range"),
+    (dict(n=0), "n >= 1"), (dict(k=0), "k >= 8"), (dict(k=60), "multiple of 8"),
     (dict(ldx=56), "ldx"), (dict(ldx=68), "ldx"), (dict(ldw=63), "ldw"), (dict(ldo=31), "ldo"),
     (dict(residual=FAKE, ldr=31), "ldr"), (dict(x=FAKE + 8), "16-byte"), (dict(w=FAKE + 2), "16-byte"),
     (dict(out=FAKE + 1), "aligned"), (dict(bias=FAKE + 2), "aligned"),
@@ -109,7 +111,8 @@ def attention_args(**over):
     (dict(k=None), "NULL k or v"), (dict(v=None), "NULL k or v"), (dict(batch=-1), "batch"), (dict(batch=65536), "batch"),
     (dict(heads=3), "multiple of kv_heads"), (dict(kv_heads=0), "kv_heads"), (dict(heads=258, kv_heads=2), "above 128"),
     (dict(head_dim=4), "head_dim"), (dict(head_dim=60), "head_dim"), (dict(head_dim=136), "head_dim"),
-    (dict(total_q=-1), "total_q"), (dict(total_k=1 << 31), "total_k"), (dict(max_q=-1), "max_q"),
+    (dict(total_q=-1), "total_q"), (dict(total_k=1 << 31), "total_k"), (dict(total_k=2 ** 31 - 1024), "total_k"),
+    (dict(total_q=2 ** 31 - 1024), "total_q"), (dict(max_q=-1), "max_q"),
     (dict(scale=float("inf")), "scale"), (dict(scale=float("nan")), "scale"), (dict(q=FAKE + 8), "16-byte"),
     (dict(k=FAKE + 2), "16-byte"), (dict(q_token_stride=257), "stride"), (dict(v_head_stride=-8), "stride"),
     (dict(k_token_stride=-128), "stride"), (dict(out_head_stride=-1), "out stride"), (dict(lse=FAKE + 2), "aligned"),
