@@ -285,15 +285,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int c = 0; c < chunks; ++c, ++seq) {
         const int n = n0 + c * 2 * cols;
         uint8_t* box = boxes + (seq & 1) * 4096;
-        float v[64];
-        tmem_ld32(acc + c * 2 * cols, reinterpret_cast<uint32_t(&)[32]>(v[0]));
-        if (!a.out_f32) tmem_ld32(acc + c * 2 * cols + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
-        tmem_ld_wait();
-        if (c == chunks - 1) {   // the accumulator is in registers: the next products may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty_l + 8u * buf);
-        }
         if (!a.tma) {
           __syncwarp();
         } else if (res) {
@@ -304,49 +295,56 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
         }
-        auto bias_act = [&](float (&x)[32], int nb) {   // the same addresses on all lanes
-          if (a.bias != nullptr) {
+        uint8_t* brow = box + lane * 128;
+        // 32 columns at a time, in a loop: the instructions of a tile's epilogue come from L2 the first time
+#pragma unroll 1
+        for (int x = 0; x < cols; x += 32) {
+          float v[32];
+          tmem_ld32(acc + c * 2 * cols + x, reinterpret_cast<uint32_t(&)[32]>(v));
+          tmem_ld_wait();
+          if (c == chunks - 1 && x == cols - 32) {   // the accumulator is in registers: the next products may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_l + 8u * buf);
+          }
+          const int nb = n + x;
+          if (a.bias != nullptr) {   // the same addresses on all lanes
             if (bias_vec && nb + 32 <= a.n) {
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
                 const float4 f = __ldg(reinterpret_cast<const float4*>(a.bias + nb + j));
-                x[j] += f.x, x[j + 1] += f.y, x[j + 2] += f.z, x[j + 3] += f.w;
+                v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
               }
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (nb + j < a.n) x[j] += __ldg(a.bias + nb + j);
+              for (int j = 0; j < 32; ++j) v[j] += __ldg(a.bias + min(nb + j, a.n - 1));
             }
           }
-          apply_act(a.act, x);
-        };
-        uint8_t* brow = box + lane * 128;
-        if (a.out_f32) {
-          bias_act(reinterpret_cast<float(&)[32]>(v[0]), n);
+          apply_act(a.act, v);
+          if (a.out_f32) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float4* p = reinterpret_cast<float4*>(brow + ((j ^ sw) << 4));
-            float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (res) {
-              const float4 r = *p;
-              o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
+            for (int j = 0; j < 8; ++j) {
+              float4* p = reinterpret_cast<float4*>(brow + ((j ^ sw) << 4));
+              float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              if (res) {
+                const float4 r = *p;
+                o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
+              }
+              *p = o;
             }
-            *p = o;
-          }
-        } else {
-          bias_act(reinterpret_cast<float(&)[32]>(v[0]), n);
-          bias_act(reinterpret_cast<float(&)[32]>(v[32]), n + 32);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4* p = reinterpret_cast<uint4*>(brow + ((j ^ sw) << 4));
-            if (res) {
-              const uint4 r = *p;
-              const float4 r0 = bf16x4_to_f32(make_uint2(r.x, r.y)), r1 = bf16x4_to_f32(make_uint2(r.z, r.w));
-              v[8 * j] += r0.x, v[8 * j + 1] += r0.y, v[8 * j + 2] += r0.z, v[8 * j + 3] += r0.w;
-              v[8 * j + 4] += r1.x, v[8 * j + 5] += r1.y, v[8 * j + 6] += r1.z, v[8 * j + 7] += r1.w;
+            for (int j = 0; j < 4; ++j) {
+              uint4* p = reinterpret_cast<uint4*>(brow + ((((x >> 3) + j) ^ sw) << 4));
+              if (res) {
+                const uint4 r = *p;
+                const float4 r0 = bf16x4_to_f32(make_uint2(r.x, r.y)), r1 = bf16x4_to_f32(make_uint2(r.z, r.w));
+                v[8 * j] += r0.x, v[8 * j + 1] += r0.y, v[8 * j + 2] += r0.z, v[8 * j + 3] += r0.w;
+                v[8 * j + 4] += r1.x, v[8 * j + 5] += r1.y, v[8 * j + 6] += r1.z, v[8 * j + 7] += r1.w;
+              }
+              *p = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                              pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
             }
-            *p = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                            pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
           }
         }
         if (!a.tma) {
