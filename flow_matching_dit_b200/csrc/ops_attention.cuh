@@ -369,10 +369,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               if (++kslot == KS) kslot = 0, kphase ^= 1u;
             }
           }
-          if (!ok) {   // only after a wait has run out: the loads under way land before the CTA leaves
-            for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) {
-            }
-          }
         }
         ++nq;
         ok = __shfl_sync(~0u, ok, 0);
@@ -801,7 +797,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   }
   __syncthreads();
-  if (KEYS && splits > 1) cluster_sync();   // nobody leaves while its part is read or its barriers are signalled
+  if (threadIdx.x == 0) op_leave(&s_abort);
+  if (KEYS && splits > 1) {
+    __syncwarp();
+    cluster_sync();   // nobody leaves while its part is read or its barriers are signalled
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -59,13 +59,6 @@ __device__ __forceinline__ bool op_wait(uint64_t* bar, uint32_t parity, volatile
   return false;
 }
 
-// The same for a whole warp: one lane polls.
-__device__ __forceinline__ bool op_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = op_wait(bar, parity, abort);
-  return __shfl_sync(~0u, ok, 0) != 0;
-}
-
 // The same for warps whose control flow should not depend on the outcome: every
 // lane polls, and after a wait has run out every wait returns at once, so that the
 // loops run to their end (on whatever the buffers hold).
@@ -73,8 +66,16 @@ __device__ __forceinline__ void op_wait_through(uint64_t* bar, uint32_t parity, 
   if (__builtin_expect(!mbar_try_wait(bar, parity), 0)) op_wait(bar, parity, abort);
 }
 
-// op_wait_warp for a barrier that other CTAs of the cluster arrive at: what they
-// wrote to shared memory before is visible then.
+// One thread at a kernel's end: after a wait has run out (only then) the copies that
+// may still be under way get 10 ms to land before the CTA leaves.
+__device__ __forceinline__ void op_leave(volatile int* abort) {
+  if (*abort)
+    for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) {
+    }
+}
+
+// For a barrier that other CTAs of the cluster arrive at, one lane polling: what they
+// wrote to shared memory before is visible then.  False once a wait has run out.
 __device__ __forceinline__ bool op_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) {
@@ -144,15 +145,6 @@ __device__ __forceinline__ void set_max_regs_dec() {
 // to be uniform the compiler moves them there one by one, which for the addresses of
 // a ring slot costs more than the multiplication itself.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(~0u, x); }
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 
 // 32 lanes x 32 (16) consecutive 32-bit TMEM columns, thread i of the warp lane base + i.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -291,13 +283,6 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
           "r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
-}
-
-// 16 bytes global -> shared, zeros where !ok (the address is then not read).
-__device__ __forceinline__ void cp_async16(void* smem_dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {

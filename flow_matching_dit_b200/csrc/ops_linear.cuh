@@ -440,12 +440,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!op_wait(&empty[stage], phase ^ 1u, &s_abort)) {
-        // only after a wait has run out: the loads under way land before the CTA leaves
-        for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) {
-        }
-        break;
-      }
+      if (!op_wait(&empty[stage], phase ^ 1u, &s_abort)) break;
       mbar_arrive_expect_tx(&full[stage], xbytes + wbytes);
       tma_load_2d(sB + stage * wbytes, &tmW, &full[stage], kb * 64, n0);
       tma_load_2d(sA + stage * xbytes, &tmX, &full[stage], kb * 64, (int)m0);
@@ -599,7 +594,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     if (splits == 1) write_rows(std::integral_constant<int, 4>());
     else write_rows(std::integral_constant<int, 1>());
   }
-  if (splits > 1) cluster_sync();   // nobody leaves while its partial tile is read
+  if (threadIdx.x == 0) op_leave(&s_abort);
+  if (splits > 1) {
+    __syncwarp();
+    cluster_sync();   // nobody leaves while its partial tile is read
+  }
 }
 
 // ------------------------------------------------------------------ planning and launches
