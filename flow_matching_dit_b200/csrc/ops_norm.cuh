@@ -32,8 +32,8 @@ struct NormArgs {
 // A warp of the team takes 128 * NU neighbouring values, so that a thread's
 // addresses differ by constants:
 //   kUnits    lane i holds the 4-value units i, i + 32, ...: 16 bytes of f32 or 8 of bf16
-//   kShifted  the same for a width that is no multiple of 4: the units lie where the addresses are aligned, and those
-//             that the row has only a part of, at its ends, are read and written value by value
+//   kShifted  the same for a width or a row stride that is no multiple of 4: the units lie where the addresses are
+//             aligned, and those that the row has only a part of, at its ends, are read and written value by value
 //   kValues   lane i holds the values i, i + 32, ...: any alignment
 // Mean and variance are sums over the registers, the second of squared deviations
 // from the first: no cancellation when the mean is large.
@@ -260,13 +260,14 @@ inline void launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
   auto aligned = [&](const void* p, long long ld, int f32) {   // rows that units of 4 values fit, all shifted alike
     return p == nullptr || ((uintptr_t)p % (f32 ? 16 : 8) == 0 && (ld - a.ldh) % 4 == 0);
   };
+  const int shift = a.ldh % 4 != 0 ? 3 : 0;   // values that a row's first unit may begin in front of it, at most
   const bool units = aligned(a.h, a.ldh, a.h_f32) && aligned(a.y, a.ldy, a.y_f32) &&
                      aligned(a.out_h, a.ldoh, a.h_f32) && aligned(a.out_u, a.ldou, a.u_f32) &&
-                     (a.dim % 4 == 0 || a.dim + 3 <= 32 * kNormThreads);   // (and with the shift the widest team holds them)
-  bool vec = units && a.dim % 4 == 0 && a.ldh % 4 == 0;
+                     a.dim + shift <= 32 * kNormThreads;   // (and with the shift the widest team holds them)
+  bool vec = units && a.dim % 4 == 0 && shift == 0;
   for (const float* p : {a.post_gain, a.post_bias, a.gate, a.pre_gain, a.pre_bias, a.scale, a.shift})
     vec = vec && ((uintptr_t)p & 15u) == 0;
-  const int width = a.dim + (units && !vec && a.dim % 4 != 0 ? 3 : 0);   // with what the shift may add in front
+  const int width = a.dim + (units ? shift : 0);   // with what the shift may add in front
   // Warps of a row: as few as hold it with 32 values a thread, so that a row of
   // up to 1024 needs no barrier; more where the rows would leave an SM fewer than 32
   // (4352 x 1024: 14 us in two warps a row, 20 in one, 19 in four).
