@@ -525,8 +525,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (mine) st = ld_cluster_f2(mapa_shared(stats + (lane & 1) * ROWS + i, (lane & (parts - 1)) >> 1));
         float m = st.x;
         for (int o = 1; o < parts; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
-        float l = f == 0.f ? 0.f : st.y * f;
+        // A part of which the row sees no key has the sum 0, and what memory holds of it does not count.  Where a score is NaN
+        // the sum is: it is kept, also where the maximum, which passes over NaN, is -infinity or far below the others'.
+        const unsigned has = __ballot_sync(~0u, st.y != 0.f);
+        const float f = st.x == -INFINITY ? st.y : ex2((st.x - m) * c);
+        float l = st.y * f;
         for (int o = 1; o < parts; o <<= 1) l += __shfl_xor_sync(~0u, l, o);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int ip = i / group, head = t.kvh * group + i - ip * group;
@@ -556,8 +559,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int p = 0; p < PB; ++p) {
-                  const float fp = __shfl_sync(~0u, f, (min(j0 + r, nj - 1) << LP) + p0 + p);
-                  const bool any = fp != 0.f;   // a part without keys holds nothing
+                  const int e = (min(j0 + r, nj - 1) << LP) + p0 + p;
+                  const float fp = __shfl_sync(~0u, f, e);
+                  const bool any = has >> e & 1u;
                   o[r].x = fmaf(any ? h[r][p].x : 0.f, fp, o[r].x), o[r].y = fmaf(any ? h[r][p].y : 0.f, fp, o[r].y);
                   o[r].z = fmaf(any ? h[r][p].z : 0.f, fp, o[r].z), o[r].w = fmaf(any ? h[r][p].w : 0.f, fp, o[r].w);
                 }

@@ -4,7 +4,7 @@ the 64-bit forms and with the tolerances of test_gpu_ops."""
 import pytest
 
 from tests.gpu_util import require_gpu
-from tests.test_gpu_ops import clean, gen, norm64, rnd, within
+from tests.test_gpu_ops import attention64, check_attention, clean, gen, norm64, rnd, within
 
 pytestmark = pytest.mark.gpu
 
@@ -55,4 +55,46 @@ def test_norm_in_place_in_wider_rows(dim):
     before = whole.clone()
     norm_residual(h, residual_scale=0.5, out_h=h)
     assert torch.equal(h, before[:, :dim] * 0.5) and torch.equal(whole[:, dim:], before[:, dim:])
+    clean()
+
+
+# ---------------------------------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("heads, kv_heads, dim", [(2, 1, 64), (8, 2, 128), (40, 2, 64), (128, 1, 64)])
+@pytest.mark.parametrize("nq", [1, 3, 150])
+@pytest.mark.parametrize("std", [1.0, 40.0])
+def test_attention_nan_inside_a_sequence(heads, kv_heads, dim, nq, std):
+    """A NaN in a query, in a visible key or value: the same outputs are NaN whichever kernel and however many parts the
+    keys are taken in, a part of which a NaN is the only score and one whose scores are far below the others' (std 40)
+    among them.  A key that causality hides does not matter."""
+    import torch
+    from flow_matching_dit_b200 import attention
+    nan = float("nan")
+    for nk, bad in ((nq, nq - 1), (129 + nq, 128 + nq), (1000 + nq, 0), (1000 + nq, 700), (3000 + nq, 2999)):
+        for what in ("q", "k", "v"):
+            g = gen(nk + nq + heads)
+            q = rnd(g, 2 * nq, heads, dim, std=std, dtype=torch.bfloat16)
+            k, v = (rnd(g, nk + 200, kv_heads, dim, std=s, dtype=torch.bfloat16) for s in (std, 1.0))
+            # the values of the other places, and NaN where the formula has it: in the rows of the query, or of those that see the key
+            ref, tol, rl, tl = attention64(q, k, v, [nq, nq], [nk, 200], [0, nk], True, dim ** -0.5)
+            sees = torch.arange(2 * nq, device="cuda") < nq
+            sees &= torch.arange(2 * nq, device="cuda") >= bad - (nk - nq)
+            group = heads // kv_heads
+            if what == "q":
+                q[nq - 1, heads - 1, 3] = nan
+                ref[nq - 1, heads - 1] = rl[nq - 1, heads - 1] = nan
+            elif what == "k":
+                k[bad, 0, dim - 1] = nan
+                ref[sees, :group] = nan
+                rl[sees, :group] = nan
+            else:
+                v[bad, kv_heads - 1, 5] = nan
+                ref[sees, heads - group:, 5] = nan
+            cu = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+            got, lse = attention(q, k, v, cu(0, nq, 2 * nq), cu(0, nk, nk + 200), max_q=nq, max_k=max(nk, 200), return_lse=True)
+            assert torch.isnan(ref).any()
+            if what == "v":   # a value may reach the queries of its sequence of which it is hidden, too
+                got[:nq, :, 5] = torch.where(sees[:nq, None] | torch.isfinite(got[:nq, :, 5]), got[:nq, :, 5], ref[:nq, :, 5].to(got.dtype))
+            within(got, ref, tol, f"{what} {nk}")
+            within(lse, rl, tl, f"lse {what} {nk}")
     clean()
