@@ -64,7 +64,7 @@ std::string shape_of(const at::Tensor& t) {
   return s + ")";
 }
 
-std::string place(int device) { return "cuda:" + std::to_string(device); }
+std::string name_of(int device) { return "cuda:" + std::to_string(device); }
 
 int device_of(const at::Tensor& t, const char* name) {
   if (!t.is_cuda()) raise(PyExc_TypeError, std::string(name) + " must be a CUDA tensor");
@@ -120,7 +120,7 @@ int64_t rows_of(const at::Tensor& t, const char* name, int device, int64_t rows,
   const std::string n(name);
   if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
     raise(PyExc_ValueError, n + " has shape " + shape_of(t) + ", expected (" + std::to_string(rows) + ", " + std::to_string(cols) + ")");
-  if (!on(t, device)) raise(PyExc_ValueError, n + " is on " + t.device().str() + ", expected " + place(device));
+  if (!on(t, device)) raise(PyExc_ValueError, n + " is on " + t.device().str() + ", expected " + name_of(device));
   const int64_t s0 = t.stride(0), s1 = t.stride(1);
   if (s1 != 1 && cols > 1) raise(PyExc_ValueError, "the rows of " + n + " must be dense");
   if (s0 < cols) {
@@ -138,7 +138,7 @@ const T* vector(PyObject* o, const char* name, int device, int64_t n, int64_t gr
   const at::ScalarType want = std::is_same<T, float>::value ? at::kFloat : at::kInt;
   if (t.scalar_type() != want || !on(t, device) || !t.is_contiguous())
     raise(PyExc_TypeError, std::string(name) + " must be a contiguous " + (want == at::kFloat ? "torch.float32" : "torch.int32") +
-                               " tensor on " + place(device));
+                               " tensor on " + name_of(device));
   if (groups < 0 ? t.dim() != 1 || t.size(0) != n : t.dim() != 2 || t.size(0) != groups || t.size(1) != n)
     raise(PyExc_ValueError, std::string(name) + " has shape " + shape_of(t) + ", expected (" +
                                 (groups < 0 ? std::to_string(n) + ",)" : std::to_string(groups) + ", " + std::to_string(n) + ")"));
@@ -161,17 +161,31 @@ at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, int device) {
   return at::detail::empty_cuda(size, type, at::Device(at::kCUDA, (c10::DeviceIndex)device), std::nullopt);
 }
 
-// The call, on the tensors' device and its current stream (or the stream given by its handle).
-template <typename Args>
-void call(int (*fn)(const Args*, void*), const Args& a, int device, PyObject* stream) {
-  const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)device));
-  void* s;
-  if (is_none(stream)) {
-    s = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-  } else {
-    s = PyLong_AsVoidPtr(stream);
-    if (s == nullptr && PyErr_Occurred()) throw Raised();
+// Where a call runs: the tensors' device and its current stream, or the stream given by
+// its handle.  That is the current stream while this lives, so that outputs made
+// meanwhile come from what the allocator keeps for it: a block of another stream's may
+// still have a reader there, and may be handed out again there before the call has run.
+struct Place {
+  c10::cuda::CUDAStream stream;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+
+  Place(PyObject* handle, int device) : stream(of(handle, (c10::DeviceIndex)device)) {
+    if (!is_none(handle) || c10::cuda::current_device() != device) guard.reset_stream(stream);
   }
+
+ private:
+  static c10::cuda::CUDAStream of(PyObject* handle, c10::DeviceIndex device) {
+    if (is_none(handle)) return c10::cuda::getCurrentCUDAStream(device);
+    void* s = PyLong_AsVoidPtr(handle);
+    if (s == nullptr && PyErr_Occurred()) throw Raised();
+    if (s == nullptr || s == cudaStreamLegacy) return c10::cuda::getDefaultCUDAStream(device);
+    return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), device);
+  }
+};
+
+template <typename Args>
+void call(int (*fn)(const Args*, void*), const Args& a, const Place& place) {
+  void* s = place.stream.stream();
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = fn(&a, s);
@@ -220,6 +234,7 @@ PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
     }
     a.activation = choice(p[3], "activation", kActivations, 5);
     a.bias = vector<float>(p[2], "bias", d, n);
+    const Place place(p[7], d);
     at::Tensor made;
     if (out != nullptr) {
       if (out->scalar_type() != type)
@@ -230,7 +245,7 @@ PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
     }
     a.x = x.data_ptr(), a.w = w.data_ptr(), a.out = (out ? *out : made).data_ptr();
     a.m = m, a.n = (int)n, a.k = (int)k;
-    call(fn_linear, a, d, p[7]);
+    call(fn_linear, a, place);
     return result(p[5], made);
   });
 }
@@ -286,6 +301,7 @@ PyObject* norm_residual(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
     const bool want_u = a.pre != 0 || scaled || shifted || !is_none(p[15]) || !is_none(p[16]);
     if (!want_h && !want_u)
       raise(PyExc_ValueError, "nothing to compute: give y, a residual_scale, pre, scale or shift");
+    const Place place(p[17], d);
     at::Tensor made_h, made_u;
     if (!is_none(p[14])) {
       const at::Tensor& t = tensor(p[14], "out_h");
@@ -312,7 +328,7 @@ PyObject* norm_residual(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
       made_h = fresh({rows, dim}, h.scalar_type(), d);
       a.out_h = made_h.data_ptr();
     }
-    call(fn_norm, a, d, p[17]);
+    call(fn_norm, a, place);
     PyObject* first = want_h ? result(p[14], made_h) : Py_NewRef(p[0]);
     PyObject* second = want_u ? result(p[15], made_u) : Py_NewRef(Py_None);
     PyObject* both = PyTuple_Pack(2, first, second);
@@ -328,7 +344,7 @@ struct Heads {
 
 Heads heads_of(const at::Tensor& t, const char* name, int device) {
   if (t.scalar_type() != at::kBFloat16 || !on(t, device))
-    raise(PyExc_TypeError, std::string(name) + " must be a bfloat16 tensor on " + place(device));
+    raise(PyExc_TypeError, std::string(name) + " must be a bfloat16 tensor on " + name_of(device));
   if (t.dim() != 3)
     raise(PyExc_ValueError, std::string(name) + " must be [tokens, heads, head_dim], got " + shape_of(t));
   Heads r = {t.size(0), t.size(1), t.size(2), t.stride(0), t.stride(1)};
@@ -377,6 +393,7 @@ PyObject* attention(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
     a.scale = is_none(p[8]) ? (float)(1.0 / std::sqrt((double)(hq.dim > 0 ? hq.dim : 1))) : number(p[8]);
     const int with_lse = PyObject_IsTrue(p[11]);
     if (with_lse < 0) throw Raised();
+    const Place place(p[12], d);
     at::Tensor made, lse;
     if (is_none(p[10])) {
       made = fresh({hq.n, hq.heads, hq.dim}, at::kBFloat16, d);
@@ -386,7 +403,7 @@ PyObject* attention(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
       lse = fresh({hq.n, hq.heads}, at::kFloat, d);
       a.lse = static_cast<float*>(lse.data_ptr());
     }
-    call(fn_attention, a, d, p[12]);
+    call(fn_attention, a, place);
     PyObject* first = result(p[10], made);
     if (!with_lse) return first;
     PyObject* second = THPVariable_Wrap(lse);

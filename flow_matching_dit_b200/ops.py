@@ -9,8 +9,10 @@ The kernels are in ``libgdit.so`` (``csrc/ops.cu``); the formulas, limits and
 error rules are those of ``include/gdit.h``.  Arguments are checked and outputs
 made in ``_binding.so`` (``csrc/binding.cpp``): a call costs the CPU 4 to 6
 microseconds, of which the launch takes 3.  Every call is one kernel on
-``stream`` (default: torch's current stream of the tensors' device), allocates
-nothing but the outputs it returns and may be captured in a CUDA graph.
+``stream`` (a handle; default: torch's current stream of the tensors' device),
+allocates nothing but the outputs it returns and may be captured in a CUDA
+graph.  Outputs belong to the stream of the call, as under
+``torch.cuda.stream``: another stream waits for it before it reads them.
 """
 
 from __future__ import annotations

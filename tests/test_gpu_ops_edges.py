@@ -98,3 +98,38 @@ def test_attention_nan_inside_a_sequence(heads, kv_heads, dim, nq, std):
             within(got, ref, tol, f"{what} {nk}")
             within(lse, rl, tl, f"lse {what} {nk}")
     clean()
+
+
+# ---------------------------------------------------------------------------------------------- streams
+
+def test_outputs_belong_to_the_stream_given():
+    """With stream= and no outputs given, these come from what the allocator keeps for that stream: not a block that the
+    current stream may still read, and not one that it may be given while the call is under way."""
+    import torch
+    from flow_matching_dit_b200 import attention, linear, norm_residual, op_status
+    g = gen(21)
+    bf = torch.bfloat16
+    x, w, h = rnd(g, 512, 512, dtype=bf), rnd(g, 512, 512, dtype=bf), rnd(g, 512, 512)
+    q, cu = x.view(512, 4, 128), torch.tensor([0, 512], dtype=torch.int32, device="cuda")
+    calls = [lambda st: (linear(x, w, stream=st),), lambda st: norm_residual(h, x, pre="rms", stream=st),
+             lambda st: attention(q, q, q, cu, cu, max_q=512, max_k=512, return_lse=True, stream=st)]
+    for handle in (0, 1):   # the default stream by its two handles
+        assert torch.equal(calls[0](handle)[0], calls[0](None)[0])
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        st = torch.cuda.Stream()
+        spare = [torch.empty_like(t) for t in want for _ in range(8)]
+        free = {t.data_ptr() for t in spare}
+        del spare   # free blocks of just these sizes on the current stream
+        got = call(st.cuda_stream)
+        assert torch.cuda.current_stream() != st
+        st.synchronize()
+        assert op_status(stream=st.cuda_stream) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        theirs = {t.data_ptr() for t in got}
+        assert not theirs & free
+        del got
+        assert not theirs & {t.data_ptr() for t in [torch.empty_like(t) for t in want for _ in range(8)]}
+        with torch.cuda.stream(st):
+            assert theirs & {t.data_ptr() for t in [torch.empty_like(t) for t in want]}
