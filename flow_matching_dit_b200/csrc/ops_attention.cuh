@@ -682,8 +682,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         if (!active) {
           wait_o();
+          __syncwarp();   // every lane has seen its phases: the arrivals let the next ones end
           if (lane == 0) mbar_arrive(sfree), mbar_arrive(&pfull[s]);
-          __syncwarp();
           continue;
         }
         tc_fence_after();

@@ -1,0 +1,26 @@
+"""Rules that the operators' kernels keep and no run can show, read from their source.  No GPU."""
+
+import os
+import re
+
+import pytest
+
+from flow_matching_dit_b200.build import PKG
+
+FILES = ("ops_attention.cuh", "ops_linear.cuh")
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_a_warp_has_converged_before_a_lane_arrives_for_it(name):
+    """In warps whose lanes each wait on a barrier for themselves, one lane's arrival speaks for the others: it lets the
+    tensor core end the next phase, and a lane that still polls for the last one would then wait for ever.  So the
+    statement in front of such an arrival is __syncwarp()."""
+    src = open(os.path.join(PKG, "csrc", name)).read()
+    lines = [re.sub(r"//.*", "", line).strip() for line in src.split("\n")]
+    lines = [line for line in lines if line]
+    found = 0
+    for i, line in enumerate(lines):
+        if re.search(r"if \(lane (== 0|< splits)\) mbar_arrive", line):
+            found += 1
+            assert lines[i - 1] == "__syncwarp();", "\n".join(lines[i - 3:i + 1])
+    assert found >= 1
