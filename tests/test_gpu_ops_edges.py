@@ -14,6 +14,31 @@ def _gpu():
     require_gpu()
 
 
+# ---------------------------------------------------------------------------------------------- linear
+
+@pytest.mark.parametrize("m", [33, 2500])
+def test_linear_gelu_is_good_relative_to_its_small_values(m):
+    """out = v Phi(v) by f32 and one bf16 value v a row.  Phi(-a) = 2^L(a): L is off by at most 2^-21 up to a = 1, 2^-17 at
+    5, 2^-15.8 up to 7, 2^-12 up to 10 and 2^-10.7 to the end, its own rounding is 2^-24 of at most 128 (2^-17) and the
+    exponential's 2^-22; those sum to less than the bounds here.  Where v is positive Phi(-v) is at most half of the
+    factor.  Results below 13 2^-126 are 0."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    n, k = 1040, 64
+    a = torch.cat([torch.logspace(-30, 0, 200), torch.linspace(1, 14, 900)]).cuda()
+    z = torch.cat([a, -a, torch.zeros(2, device="cuda")]).bfloat16()
+    z = z.repeat(m // len(z) + 1)[:m] if m > len(z) else z[torch.linspace(0, len(z) - 1, m).long().cuda()]
+    x, w = (torch.zeros(r, k, device="cuda", dtype=torch.bfloat16) for r in (m, n))
+    x[:, 0], w[:, 0] = z, 1
+    got = linear(x, w, activation="gelu", out_dtype=torch.float32)
+    v = z.double()[:, None].expand(m, n)
+    ref = 0.5 * v * torch.erfc(-v * 0.5 ** 0.5)
+    a = v.abs()
+    rel = torch.where((v > 0) | (a <= 1), 2.0 ** -19, torch.where(a <= 5, 2.0 ** -16, torch.where(a <= 7, 2.0 ** -14.5, 2.0 ** -10)))
+    within(got, ref, rel * ref.abs() + 13 * 2.0 ** -126, "gelu")
+    clean()
+
+
 # ---------------------------------------------------------------------------------------------- norm_residual
 
 def padded(g, rows, dim, pad, dtype, std=1.0):
