@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -53,9 +54,14 @@ PyObject* guarded(F&& f) {
 
 bool is_none(PyObject* o) { return o == Py_None; }
 
+// Every tensor of a call goes through here.
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, std::string(name) + " must be a tensor, got " + Py_TYPE(o)->tp_name);
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (at::GradMode::is_enabled() && t.requires_grad())
+    raise(PyExc_RuntimeError, std::string(name) + " requires a gradient, which this operator does not have: call it under torch.no_grad() or with " +
+                                  name + ".detach()");
+  return t;
 }
 
 std::string shape_of(const at::Tensor& t) {

@@ -12,7 +12,10 @@ microseconds, of which the launch takes 3.  Every call is one kernel on
 ``stream`` (a handle; default: torch's current stream of the tensors' device),
 allocates nothing but the outputs it returns and may be captured in a CUDA
 graph.  Outputs belong to the stream of the call, as under
-``torch.cuda.stream``: another stream waits for it before it reads them.
+``torch.cuda.stream``: another stream waits for it before it reads them.  The
+operators have no backward pass: where gradients are on, a tensor that requires
+one is refused (RuntimeError); ``torch.no_grad()`` or ``detach()`` says that none
+is wanted.
 """
 
 from __future__ import annotations

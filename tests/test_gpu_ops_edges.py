@@ -158,3 +158,33 @@ def test_outputs_belong_to_the_stream_given():
         assert not theirs & {t.data_ptr() for t in [torch.empty_like(t) for t in want for _ in range(8)]}
         with torch.cuda.stream(st):
             assert theirs & {t.data_ptr() for t in [torch.empty_like(t) for t in want]}
+
+
+# ---------------------------------------------------------------------------------------------- autograd
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """No gradient is dropped silently: every tensor of each operator, outputs among them."""
+    import torch
+    from flow_matching_dit_b200 import attention, linear, norm_residual
+    bf = torch.bfloat16
+    mat = lambda dt=bf: torch.ones(8, 64, device="cuda", dtype=dt)  # noqa: E731
+    vec = lambda: torch.ones(64, device="cuda")  # noqa: E731
+    heads, cu = lambda: torch.ones(8, 1, 64, device="cuda", dtype=bf), torch.tensor([0, 8], dtype=torch.int32, device="cuda")  # noqa: E731
+    calls = [(linear, dict(x=mat(), w=torch.ones(64, 64, device="cuda", dtype=bf), bias=vec(), residual=mat(), out=mat()), {}),
+             (norm_residual, dict(h=mat(torch.float32), y=mat(), post_gain=vec(), post_bias=vec(), gate=vec(), pre_gain=vec(),
+                                  pre_bias=vec(), scale=vec(), shift=vec(), out_h=mat(torch.float32), out_u=mat()),
+              dict(post="layer", pre="layer")),
+             (attention, dict(q=heads(), k=heads(), v=heads(), out=heads()), dict(cu_q=cu, cu_k=cu, max_q=8, max_k=8))]
+    for f, tensors, rest in calls:
+        f(**tensors, **rest)
+        for name in tensors:
+            with_grad = {**tensors, name: tensors[name].clone().requires_grad_()}
+            with pytest.raises(RuntimeError, match=f"{name} requires a gradient"):
+                f(**with_grad, **rest)
+            with torch.no_grad():
+                f(**with_grad, **rest)
+            f(**{**tensors, name: with_grad[name].detach()}, **rest)
+            if "out" not in name:
+                with torch.inference_mode():
+                    f(**with_grad, **rest)
+    clean()
