@@ -209,9 +209,13 @@ void expect(Py_ssize_t n, Py_ssize_t want) {
   if (fn_linear == nullptr) raise(PyExc_RuntimeError, "the library's entry points are not set");
 }
 
+// An output: the tensor given, whose version counts the write (so that autograd sees that a
+// tensor which it has kept is no longer what it was), or the one made here.
 PyObject* result(PyObject* given, const at::Tensor& made) {
-  if (!is_none(given)) return Py_NewRef(given);
-  return THPVariable_Wrap(made);
+  if (is_none(given)) return THPVariable_Wrap(made);
+  const at::Tensor& t = THPVariable_Unpack(given);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return Py_NewRef(given);
 }
 
 // linear(x, w, bias, activation, residual, out, out_dtype, stream)

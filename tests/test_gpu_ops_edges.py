@@ -188,3 +188,27 @@ def test_tensors_that_require_a_gradient_are_refused():
                 with torch.inference_mode():
                     f(**with_grad, **rest)
     clean()
+
+
+def test_writes_into_given_tensors_are_seen_by_autograd():
+    """A tensor that autograd has kept and an operator has written since: its backward pass says so."""
+    import torch
+    from flow_matching_dit_b200 import attention, linear, norm_residual
+    bf = torch.bfloat16
+    x, h, cu = (torch.ones(8, 64, device="cuda", dtype=bf), torch.ones(8, 64, device="cuda"),
+                torch.tensor([0, 8], dtype=torch.int32, device="cuda"))
+    q, w = x.view(8, 1, 64), torch.ones(64, 64, device="cuda", dtype=bf)
+    for call, shape, dtype in ((lambda t: linear(x, w, out=t), (8, 64), bf), (lambda t: norm_residual(h, x, out_h=t), (8, 64), h.dtype),
+                               (lambda t: norm_residual(h, x, pre="rms", out_u=t), (8, 64), bf),
+                               (lambda t: attention(q, q, q, cu, cu, max_q=8, max_k=8, out=t), (8, 1, 64), bf)):
+        out = torch.ones(shape, device="cuda", dtype=dtype)
+        leaf = torch.ones(shape, device="cuda", dtype=dtype, requires_grad=True)
+        product = leaf * out
+        before = out._version
+        call(out)
+        assert out._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            product.sum().backward()
+        with torch.inference_mode():
+            call(torch.ones(shape, device="cuda", dtype=dtype))   # such tensors have no version
+    clean()
