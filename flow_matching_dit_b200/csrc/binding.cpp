@@ -232,6 +232,8 @@ PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
     gdit_linear_args a = {};
     a.ldx = rows_of(x, "x", d, m, k);
     a.ldw = rows_of(w, "w", d, n, k);
+    if (m <= 1) a.ldx = k;   // one row: its stride addresses nothing, and need not be the multiple of 8 that k is
+    if (n <= 1) a.ldw = k;
     const at::Tensor *res = is_none(p[4]) ? nullptr : &tensor(p[4], "residual"), *out = is_none(p[5]) ? nullptr : &tensor(p[5], "out");
     const at::ScalarType type = !is_none(p[6]) ? dtype(p[6], "out_dtype") : out ? out->scalar_type() : res ? res->scalar_type() : at::kBFloat16;
     a.out_dtype = code_of(type, "out_dtype");

@@ -4,7 +4,7 @@ the 64-bit forms and with the tolerances of test_gpu_ops."""
 import pytest
 
 from tests.gpu_util import require_gpu
-from tests.test_gpu_ops import attention64, check_attention, clean, gen, norm64, rnd, within
+from tests.test_gpu_ops import attention64, check_attention, clean, gen, linear64, norm64, rnd, within
 
 pytestmark = pytest.mark.gpu
 
@@ -36,6 +36,24 @@ def test_linear_gelu_is_good_relative_to_its_small_values(m):
     a = v.abs()
     rel = torch.where((v > 0) | (a <= 1), 2.0 ** -19, torch.where(a <= 5, 2.0 ** -16, torch.where(a <= 7, 2.0 ** -14.5, 2.0 ** -10)))
     within(got, ref, rel * ref.abs() + 13 * 2.0 ** -126, "gelu")
+    clean()
+
+
+def test_linear_one_row_of_any_stride():
+    """One row of x, or of w, whose stride addresses nothing."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    g = gen(9)
+    k = 72
+    for m, n in ((1, 40), (6, 1), (1, 1)):
+        x, w = (rnd(g, rows + 1, k + 9, dtype=torch.bfloat16)[:rows, :k] if rows == 1 else rnd(g, rows, k, dtype=torch.bfloat16)
+                for rows in (m, n))
+        assert m > 1 or x.stride(0) == k + 9
+        got = linear(x, w, activation="silu", out_dtype=torch.float32)
+        within(got, *linear64(x, w, None, "silu", None, torch.float32), f"{m} x {n}")
+    two = rnd(g, 2, k + 9, dtype=torch.bfloat16)[:, :k]
+    with pytest.raises(RuntimeError):
+        linear(two, rnd(g, 8, k, dtype=torch.bfloat16))
     clean()
 
 
