@@ -4,7 +4,7 @@
 ``csrc/gdit.cu`` (the action head) and ``csrc/ops.cu`` (the operators) with nvcc
 into ``flow_matching_dit_b200/libgdit.so``, and ``csrc/binding.cpp`` (the
 operators' Python calls) with the host compiler against torch's headers into
-``_binding.so``.  With ``checked=True`` the library goes into ``libgdit_checked.so``, the range-checked build
+``_binding.so``.  With ``checked=True`` the library alone goes into ``libgdit_checked.so``, the range-checked build
 (``-DGDIT_CHECKED=1``: guard bands around device allocations, index checks in
 the kernels).  nvcc cross-compiles, so this works on a machine without a GPU.
 """
@@ -78,15 +78,28 @@ def _run(cmd: list, tmp: str, out: str, verbose: bool) -> None:
     os.replace(tmp, out)
 
 
+def binding_possible() -> bool:
+    """Whether torch and Python's headers are here, which the binding needs and the library does not."""
+    import importlib.util
+    import sysconfig
+    return importlib.util.find_spec("torch") is not None and \
+        os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
-    """Builds what is not up to date; returns the library's path."""
+    """Builds what is not up to date; returns the library's path.  The operators' binding is built with the library, not
+    with its checked form, and left out (and said so) where torch or Python's headers are missing: the operators' Python
+    calls then raise, all else works."""
     out = LIB_CHECKED if checked else LIB
     if force or not up_to_date(out):
         tmp = out + ".tmp"
         _run(command(tmp, checked), tmp, out, verbose)
-    if force or not binding_up_to_date():
-        tmp = BINDING + ".tmp"
-        _run(binding_command(tmp), tmp, BINDING, verbose)
+    if not checked and (force or not binding_up_to_date()):
+        if binding_possible():
+            tmp = BINDING + ".tmp"
+            _run(binding_command(tmp), tmp, BINDING, verbose)
+        else:
+            print("torch or Python.h not found: the operators' Python calls are not built", file=sys.stderr)
     return out
 
 
