@@ -1,4 +1,5 @@
 // C ABI of the operators (see include/gdit.h): argument checks and launches.
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -159,7 +160,9 @@ int gdit_attention(const gdit_attention_args* p, void* cuda_stream) {
             "total_q %lld or total_k %lld out of range", (long long)p->total_q, (long long)p->total_k);
     REQUIRE(p->total_q * (p->heads / p->kv_heads) <= kMaxRows - 256, "total_q * heads / kv_heads out of range");
     REQUIRE(p->max_q >= 0 && p->max_k >= 0, "max_q %d, max_k %d", p->max_q, p->max_k);
+    const float scale_log2 = p->scale * 1.4426950408889634f;
     REQUIRE(std::isfinite(p->scale), "scale must be finite");
+    REQUIRE(std::isfinite(scale_log2), "scale %g out of range", p->scale);
     if (p->batch == 0 || p->total_q == 0) return;
     REQUIRE(p->q && p->out && p->cu_q && p->cu_k, "NULL q, out, cu_q or cu_k");
     REQUIRE(p->total_k == 0 || (p->k && p->v), "NULL k or v");
@@ -185,9 +188,8 @@ int gdit_attention(const gdit_attention_args* p, void* cuda_stream) {
     a.v_t = p->v_token_stride, a.v_h = p->v_head_stride, a.o_t = p->out_token_stride, a.o_h = p->out_head_stride;
     a.batch = p->batch, a.heads = p->heads, a.kv_heads = p->kv_heads, a.dim = p->head_dim;
     a.max_q = p->max_q, a.max_k = p->max_k, a.causal = p->causal != 0;
-    a.scale_log2 = p->scale * 1.4426950408889634f;
-    // a score of -infinity (a masked one) times 0 would be NaN; this scale leaves every other score at 0
-    if (std::fabs(a.scale_log2) < 1e-30f) a.scale_log2 = 1e-30f;
+    // a score of -infinity (a masked one) times 0 would be NaN; the smallest scale leaves all but the largest others at 0
+    a.scale_log2 = std::fabs(scale_log2) < FLT_MIN ? FLT_MIN : scale_log2;
     launch_attention(a, sms, (cudaStream_t)cuda_stream);
   });
 }

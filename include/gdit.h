@@ -478,7 +478,7 @@ int gdit_norm_residual(const gdit_norm_args* a, void* cuda_stream);
  * heads a multiple of kv_heads; heads / kv_heads <= 128; head_dim a multiple
  * of 8 in [8, 128]; q, k, v 16-byte aligned with strides that are multiples of
  * 8; total_k and total_q * heads / kv_heads up to 2^31 - 1281; batch in
- * [0, 65535]; scale finite. */
+ * [0, 65535]; scale up to 2.3e38 in magnitude. */
 typedef struct {
   const void* q;
   const void* k;

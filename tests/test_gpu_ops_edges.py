@@ -143,6 +143,22 @@ def test_attention_nan_inside_a_sequence(heads, kv_heads, dim, nq, std):
     clean()
 
 
+@pytest.mark.parametrize("nq", [1, 200])
+@pytest.mark.parametrize("size, scale", [(2.0 ** 60, 2.0 ** -122), (2.0 ** 55, -2.0 ** -111), (2.0 ** -60, 2.0 ** 120), (1.0, 0.0)])
+def test_attention_scales_far_from_one(nq, size, scale):
+    """Queries and keys of magnitude `size`, whose scores the scale brings back to ordinary ones."""
+    import torch
+    from flow_matching_dit_b200 import attention
+    g = gen(nq)
+    q, k, v = (rnd(g, n, 2, 64, dtype=torch.bfloat16) for n in (nq, 300, 300))
+    cu = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    got, lse = attention(q * size, k * size, v, cu(0, nq), cu(0, 300), max_q=nq, max_k=300, scale=scale, return_lse=True)
+    ref, tol, rl, tl = attention64(q, k, v, [nq], [300], [0], True, scale * size ** 2)
+    within(got, ref, tol, "out")
+    within(lse, rl, tl, "lse")
+    clean()
+
+
 # ---------------------------------------------------------------------------------------------- streams
 
 def test_outputs_belong_to_the_stream_given():
