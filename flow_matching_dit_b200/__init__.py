@@ -302,6 +302,20 @@ def debug_skinny_plan(M: int, N: int, K: int, num_sms: int = 148):
     return dict(zip(("mt", "nu", "stages", "ctas", "smem_bytes"), (o.value for o in out)))
 
 
+def debug_linear_plan(m: int, n: int, k: int, out_dtype: int = GDIT_BF16, residual: bool = False, aligned: bool = True,
+                      num_sms: int = 148):
+    """The kernel that ``linear`` takes for [m, k] x [n, k]^T (gdit_debug_linear_plan; num_sms 0: on the current
+    device): dict(pair, bn, splits).  aligned: whether TMA can address out and residual, whose rows are dense."""
+    size, fake = (4 if out_dtype == GDIT_F32 else 2), 1 << 20
+    out = fake if aligned else fake + size
+    ld = -(-n * size // 16) * 16 // size if aligned else n
+    a = _lib.gdit_linear_args(x=fake, w=fake, out=out, residual=out if residual else None, m=m, n=n, k=k, ldx=k, ldw=k,
+                              ldo=ld, ldr=ld, out_dtype=out_dtype)
+    r = [ctypes.c_int() for _ in range(3)]
+    check(_lib.gdit_debug_linear_plan(ctypes.byref(a), int(num_sms), *[ctypes.byref(v) for v in r]))
+    return {"pair": bool(r[0].value), "bn": r[1].value, "splits": r[2].value}
+
+
 def debug_wait_expiry(device: int = 0, limit_ns: int = 1_000_000) -> int:
     """Status of one bounded wait on an mbarrier that nothing arrives at
     (gdit_debug_wait_expiry): GDIT_ETIMEOUT is the expected result."""

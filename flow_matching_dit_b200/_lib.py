@@ -111,6 +111,7 @@ _SIGS = {
     "gdit_check_canaries": (_I, [_P, ctypes.POINTER(ctypes.c_longlong)]),
     "gdit_debug_poke_guard": (_I, [_P, _I]),
     "gdit_linear": (_I, [ctypes.POINTER(gdit_linear_args), _P]),
+    "gdit_debug_linear_plan": (_I, [ctypes.POINTER(gdit_linear_args), _I] + [ctypes.POINTER(_I)] * 3),
     "gdit_norm_residual": (_I, [ctypes.POINTER(gdit_norm_args), _P]),
     "gdit_attention": (_I, [ctypes.POINTER(gdit_attention_args), _P]),
     "gdit_op_status": (_I, [_I, _P]),
@@ -254,6 +255,10 @@ def gdit_norm_residual(args, stream):
 
 def gdit_attention(args, stream):
     return lib().gdit_attention(args, stream)
+
+
+def gdit_debug_linear_plan(*a):
+    return lib().gdit_debug_linear_plan(*a)
 
 
 def gdit_op_status(device, stream):

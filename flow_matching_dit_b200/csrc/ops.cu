@@ -62,6 +62,36 @@ constexpr int64_t kMaxStride = (int64_t)1 << 40;
 // Rows, columns and keys: the last tile's end still fits 32 bits.
 constexpr int64_t kMaxRows = (int64_t)INT32_MAX - 1024;
 
+// Checks the arguments of a product; false where there is nothing to do.
+bool linear_args(const gdit_linear_args* p, LinearArgs& a) {
+  REQUIRE(p != nullptr, "NULL arguments");
+  REQUIRE(p->m >= 0 && p->m <= kMaxRows, "m %lld out of range", (long long)p->m);
+  REQUIRE(p->n >= 1 && p->k >= 8 && p->k % 8 == 0, "need n >= 1 and k >= 8, a multiple of 8 (n %d, k %d)", p->n, p->k);
+  REQUIRE(p->n <= kMaxRows && p->k <= kMaxRows, "n %d or k %d out of range", p->n, p->k);
+  REQUIRE(is_dtype(p->out_dtype), "out_dtype %d", p->out_dtype);
+  REQUIRE(p->activation >= GDIT_ACT_NONE && p->activation <= GDIT_ACT_SILU, "activation %d", p->activation);
+  if (p->m == 0) return false;
+  REQUIRE(p->x && p->w && p->out, "NULL matrix");
+  const int es = size_of(p->out_dtype);
+  REQUIRE(p->ldx >= p->k && p->ldx % 8 == 0 && p->ldx <= kMaxStride, "ldx %lld: at least k and a multiple of 8", (long long)p->ldx);
+  REQUIRE(p->ldw >= p->k && p->ldw % 8 == 0 && p->ldw <= kMaxStride, "ldw %lld: at least k and a multiple of 8", (long long)p->ldw);
+  REQUIRE(p->ldo >= p->n && p->ldo <= kMaxStride, "ldo %lld below n", (long long)p->ldo);
+  REQUIRE(p->residual == nullptr || (p->ldr >= p->n && p->ldr <= kMaxStride), "ldr %lld below n", (long long)p->ldr);
+  REQUIRE(aligned_to(p->x, 16) && aligned_to(p->w, 16), "x and w must be 16-byte aligned");
+  REQUIRE(aligned_to(p->out, es) && aligned_to(p->residual, es) && aligned_to(p->bias, 4),
+          "bias, residual or out not aligned to its element");
+  a.x = static_cast<const __nv_bfloat16*>(p->x);
+  a.w = static_cast<const __nv_bfloat16*>(p->w);
+  a.bias = p->bias;
+  a.residual = p->residual;
+  a.out = p->out;
+  a.m = p->m, a.ldx = p->ldx, a.ldw = p->ldw, a.ldr = p->ldr, a.ldo = p->ldo;
+  a.n = p->n, a.k = p->k;
+  a.out_f32 = p->out_dtype == GDIT_F32;
+  a.act = p->activation;
+  return true;
+}
+
 __global__ void clear_status_kernel(unsigned bits) { atomicAnd(&g_op_status, ~bits); }
 
 }  // namespace
@@ -70,34 +100,25 @@ extern "C" {
 
 int gdit_linear(const gdit_linear_args* p, void* cuda_stream) {
   return guarded_op([&] {
-    REQUIRE(p != nullptr, "NULL arguments");
-    REQUIRE(p->m >= 0 && p->m <= kMaxRows, "m %lld out of range", (long long)p->m);
-    REQUIRE(p->n >= 1 && p->k >= 8 && p->k % 8 == 0, "need n >= 1 and k >= 8, a multiple of 8 (n %d, k %d)", p->n, p->k);
-    REQUIRE(p->n <= kMaxRows && p->k <= kMaxRows, "n %d or k %d out of range", p->n, p->k);
-    REQUIRE(is_dtype(p->out_dtype), "out_dtype %d", p->out_dtype);
-    REQUIRE(p->activation >= GDIT_ACT_NONE && p->activation <= GDIT_ACT_SILU, "activation %d", p->activation);
-    if (p->m == 0) return;
-    REQUIRE(p->x && p->w && p->out, "NULL matrix");
-    const int es = size_of(p->out_dtype);
-    REQUIRE(p->ldx >= p->k && p->ldx % 8 == 0 && p->ldx <= kMaxStride, "ldx %lld: at least k and a multiple of 8", (long long)p->ldx);
-    REQUIRE(p->ldw >= p->k && p->ldw % 8 == 0 && p->ldw <= kMaxStride, "ldw %lld: at least k and a multiple of 8", (long long)p->ldw);
-    REQUIRE(p->ldo >= p->n && p->ldo <= kMaxStride, "ldo %lld below n", (long long)p->ldo);
-    REQUIRE(p->residual == nullptr || (p->ldr >= p->n && p->ldr <= kMaxStride), "ldr %lld below n", (long long)p->ldr);
-    REQUIRE(aligned_to(p->x, 16) && aligned_to(p->w, 16), "x and w must be 16-byte aligned");
-    REQUIRE(aligned_to(p->out, es) && aligned_to(p->residual, es) && aligned_to(p->bias, 4),
-            "bias, residual or out not aligned to its element");
-    const int sms = current_sms();
     LinearArgs a;
-    a.x = static_cast<const __nv_bfloat16*>(p->x);
-    a.w = static_cast<const __nv_bfloat16*>(p->w);
-    a.bias = p->bias;
-    a.residual = p->residual;
-    a.out = p->out;
-    a.m = p->m, a.ldx = p->ldx, a.ldw = p->ldw, a.ldr = p->ldr, a.ldo = p->ldo;
-    a.n = p->n, a.k = p->k;
-    a.out_f32 = p->out_dtype == GDIT_F32;
-    a.act = p->activation;
-    launch_linear(a, sms, (cudaStream_t)cuda_stream);
+    if (!linear_args(p, a)) return;
+    launch_linear(a, current_sms(), (cudaStream_t)cuda_stream);
+  });
+}
+
+int gdit_debug_linear_plan(const gdit_linear_args* p, int num_sms, int* pair, int* bn, int* splits) {
+  return guarded_op([&] {
+    LinearArgs a;
+    REQUIRE(pair && bn && splits, "NULL output");
+    REQUIRE(num_sms == 0 || num_sms >= 8, "num_sms %d: 0, or at least 8", num_sms);   // (a cluster of 8)
+    REQUIRE(linear_args(p, a), "no rows");
+    SplitSlots slots = {{0}};
+    for (int n = 1; n <= 8; ++n) slots.of[n] = num_sms / n * n;
+    const int sms = num_sms > 0 ? num_sms : current_sms();
+    const LinearPlan plan = plan_linear(a, sms, num_sms > 0 ? slots : split_slots(sms));
+    *pair = plan.pair_bn > 0;
+    *bn = plan.pair_bn > 0 ? plan.pair_bn : plan.split.bn;
+    *splits = plan.pair_bn > 0 ? 1 : plan.split.splits;
   });
 }
 

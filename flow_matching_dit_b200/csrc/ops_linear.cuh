@@ -696,9 +696,8 @@ inline const SplitSlots& split_slots(int sms) {
 // pair_time.  The coefficients fit the times of 80 sizes (1 to 16384 rows, 16 to 8192
 // columns, K of 32 to 8192, aligned and odd) in up to 23 plans each; the plan chosen took
 // 3 % longer than the best one on average, 24 % at most.
-inline SplitPlan plan_split(long long m, int n, int k, int sms) {
+inline SplitPlan plan_split(long long m, int n, int k, const SplitSlots& slots) {
   SplitPlan p = {};
-  const SplitSlots& slots = split_slots(sms);
   const int nkb = (k + 63) / 64;
   const long long mt = (m + 127) / 128;
   p.xrows = 8;
@@ -730,20 +729,29 @@ inline double pair_time(const LinearArgs& a, int bn, int sms) {
   return 1.2 + std::max(rounds * products + epilogue, rounds * std::max(products, epilogue));
 }
 
-inline void launch_linear(LinearArgs& a, int sms, cudaStream_t s) {
+struct LinearPlan {
+  int pair_bn;       // tile width of the pair kernel, or 0 for the split kernel
+  SplitPlan split;
+};
+
+// (sets a.tma, too)
+inline LinearPlan plan_linear(LinearArgs& a, int sms, const SplitSlots& slots) {
   const int es = a.out_f32 ? 4 : 2;
   auto tma_ok = [&](const void* p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld * es % 16 == 0; };
   a.tma = tma_ok(a.out, a.ldo) && (a.residual == nullptr || tma_ok(a.residual, a.ldr));
-  const SplitPlan p = plan_split(a.m, a.n, a.k, sms);
+  LinearPlan p = {0, plan_split(a.m, a.n, a.k, slots)};
   const double wide = pair_time(a, 256, sms), narrow = pair_time(a, 128, sms);
-  if (std::min(wide, narrow) < p.time) {
-    if (wide < narrow) launch_linear_pair<256>(a, sms, s);
-    else launch_linear_pair<128>(a, sms, s);
-    return;
-  }
-  if (p.bn == 128) launch_linear_split<128>(a, p, s);
-  else if (p.bn == 64) launch_linear_split<64>(a, p, s);
-  else launch_linear_split<32>(a, p, s);
+  if (std::min(wide, narrow) < p.split.time) p.pair_bn = wide < narrow ? 256 : 128;
+  return p;
+}
+
+inline void launch_linear(LinearArgs& a, int sms, cudaStream_t s) {
+  const LinearPlan p = plan_linear(a, sms, split_slots(sms));
+  if (p.pair_bn == 256) launch_linear_pair<256>(a, sms, s);
+  else if (p.pair_bn == 128) launch_linear_pair<128>(a, sms, s);
+  else if (p.split.bn == 128) launch_linear_split<128>(a, p.split, s);
+  else if (p.split.bn == 64) launch_linear_split<64>(a, p.split, s);
+  else launch_linear_split<32>(a, p.split, s);
 }
 
 }  // namespace gdit

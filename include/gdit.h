@@ -415,6 +415,15 @@ typedef struct {
 
 int gdit_linear(const gdit_linear_args* a, void* cuda_stream);
 
+/* The plan of gdit_linear for these arguments on num_sms SMs (at least 8; a
+ * host computation, no GPU needed: as if clusters of any size filled them), or
+ * with num_sms 0 on the current device: *pair = 1 for the kernel on pairs of
+ * CTAs, 0 for the one that cuts k over a cluster; *bn = columns of a tile;
+ * *splits = parts of k.  Pointers are looked at for their alignment, not
+ * followed.  GDIT_EINVAL for arguments that gdit_linear refuses and for m = 0.
+ * For tests. */
+int gdit_debug_linear_plan(const gdit_linear_args* a, int num_sms, int* pair, int* bn, int* splits);
+
 /* Row by row (row r, width dim, group c = row_group[r]):
  *   h' = residual_scale h + gate * post(y)      written to out_h
  *   u  = pre(h') (1 + scale) + shift            written to out_u

@@ -1,10 +1,12 @@
 """The operators where their layouts, values or callers are unusual, against
 the 64-bit forms and with the tolerances of test_gpu_ops."""
 
+import math
+
 import pytest
 
 from tests.gpu_util import require_gpu
-from tests.test_gpu_ops import attention64, check_attention, clean, gen, linear64, norm64, rnd, within
+from tests.test_gpu_ops import U16, act64, attention64, check_linear, clean, gen, linear64, norm64, rnd, within
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +56,81 @@ def test_linear_one_row_of_any_stride():
     two = rnd(g, 2, k + 9, dtype=torch.bfloat16)[:, :k]
     with pytest.raises(RuntimeError):
         linear(two, rnd(g, 8, k, dtype=torch.bfloat16))
+    clean()
+
+
+PAIR_SIZES = [(4100, 4104, 2048, 256), (4100, 4103, 2048, 256), (4100, 1032, 520, 128), (4100, 1030, 520, 128)]
+
+
+def on_pairs(m, n, k, bn, dt, residual=True, aligned=None):
+    """Sizes that run on pairs of CTAs with tiles of bn columns, by the planner."""
+    import torch
+    from flow_matching_dit_b200 import GDIT_BF16, GDIT_F32, debug_linear_plan
+    if aligned is None:
+        aligned = n * (4 if dt == torch.float32 else 2) % 16 == 0
+    plan = debug_linear_plan(m, n, k, GDIT_F32 if dt == torch.float32 else GDIT_BF16, residual, aligned, num_sms=0)
+    assert plan == {"pair": True, "bn": bn, "splits": 1}
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("bias, residual", [(False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("m, n, k, bn", PAIR_SIZES)
+def test_linear_pair_epilogues(m, n, k, bn, act, out, bias, residual):
+    """Each epilogue of the pair kernel: outputs by TMA boxes and, where rows begin anywhere, by words; last tiles of 4 rows
+    and of 8, 7 or 6 columns."""
+    import torch
+    on_pairs(m, n, k, bn, {"bf16": torch.bfloat16, "f32": torch.float32}[out], residual)
+    check_linear(m, n, k, act, out, bias, residual, seed=5, std=2.0)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("offset, pad", [(8, 16), (0, 8), (1, 5), (3, 0)])
+@pytest.mark.parametrize("m, n, k, bn", [(4100, 4104, 2048, 256), (4100, 1032, 520, 128)])
+def test_linear_pair_strided_and_in_place(m, n, k, bn, out, offset, pad):
+    """Outputs inside wider rows, aligned for TMA and not, the residual another tensor or the output itself; what lies around
+    them stays as it was."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    g = gen(n + offset)
+    x, w = rnd(g, m, k, dtype=torch.bfloat16), rnd(g, n, k, std=k ** -0.5, dtype=torch.bfloat16)
+    b = rnd(g, n)
+    wide = rnd(g, m, offset + n + pad, dtype=dt)
+    size = wide.element_size()
+    aligned = offset * size % 16 == 0 and wide.shape[1] * size % 16 == 0
+    on_pairs(m, n, k, bn, dt, True, aligned)
+    view, before = wide[:, offset:offset + n], wide.clone()
+    other = rnd(g, m, offset + n + pad, dtype=dt)[:, offset:offset + n]
+    for residual in (other, None, view):
+        ref, tol = linear64(x, w, b, "silu", None if residual is None else residual.clone(), dt)
+        assert linear(x, w, b, activation="silu", residual=residual, out=view) is view
+        within(view, ref, tol)
+        assert torch.equal(wide[:, :offset], before[:, :offset]) and torch.equal(wide[:, offset + n:], before[:, offset + n:])
+    clean()
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_pair_activations_far_out(act, out):
+    """Arguments from tiny to far outside and NaN, one a row, beside rows of another size: no row reaches another."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    m, n, k = 4100, 4104, 2048
+    on_pairs(m, n, k, 256, dt, False)
+    z = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-4, -1e-4, 0.5, -0.5, 3.0, -3.0, 6.0, -6.0, 20.0, -20.0, 42.0, -42.0, 60.0, -60.0,
+                      100.0, -100.0, 1e4, -1e4, 1e12, -1e12, 1e20, -1e20, 3e38, -3e38, float("nan"), -2.0, 90.0], device="cuda").bfloat16()
+    z = z.repeat(m // len(z) + 1)[:m]
+    x, w = torch.zeros(m, k, device="cuda", dtype=torch.bfloat16), torch.zeros(n, k, device="cuda", dtype=torch.bfloat16)
+    x[:, 1000], w[:, 1000] = z, 1
+    got = linear(x, w, activation=act, out_dtype=dt)
+    v = z.double()[:, None].expand(m, n)
+    ref = act64(v, act) if act != "gelu_tanh" else v * torch.sigmoid(2 * (2 / math.pi) ** 0.5 * (v + 0.044715 * v ** 3))
+    # exponentials and reciprocals to a few 2^-22, arguments of 2 (2/pi)^0.5 log2(e) (v + 0.044715 v^3) < 62 to 2^-23 of them, nothing
+    # below 2^-62 of the argument; then the output's half step
+    tol = 2.0 ** -16 * ref.abs() + 2.0 ** -61 * v.abs().clamp_max(64) + 1e-30
+    within(got, ref, tol + (U16 if out == "bf16" else 0) * (ref.abs() + tol), act)
     clean()
 
 
