@@ -134,6 +134,20 @@ def test_linear_pair_activations_far_out(act, out):
     clean()
 
 
+@pytest.mark.parametrize("m, n, k", [(140000, 16400, 8), (140001, 16401, 16), (2200, 1000003, 8)])
+def test_linear_outputs_past_31_bits(m, n, k):
+    """More than 2^31 outputs: the last ones lie where they should, bias and residual too."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    g = gen(m)
+    x, w, b = rnd(g, m, k, dtype=torch.bfloat16), rnd(g, n, k, dtype=torch.bfloat16), rnd(g, n)
+    out = torch.full((m, n), 3.0, device="cuda", dtype=torch.bfloat16)
+    assert m * n > 2 ** 31 and linear(x, w, b, residual=out, out=out) is out
+    for rows in (slice(0, 40), slice(m - 40, m)):
+        within(out[rows], *linear64(x[rows], w, b, "none", torch.full((40, n), 3.0, device="cuda"), torch.bfloat16), f"rows {rows}")
+    clean()
+
+
 # ---------------------------------------------------------------------------------------------- norm_residual
 
 def padded(g, rows, dim, pad, dtype, std=1.0):
@@ -236,6 +250,119 @@ def test_attention_scales_far_from_one(nq, size, scale):
     clean()
 
 
+def spread(t, how):
+    """The values of t [tokens, heads, dim] in another layout."""
+    import torch
+    n, h, d = t.shape
+    if how == "heads first":
+        return t.transpose(0, 1).contiguous().transpose(0, 1)
+    if how == "wide":        # room behind each head and each token
+        big = torch.zeros(n, h + 1, d + 24, device="cuda", dtype=t.dtype)
+    else:                    # "odd": rows that begin anywhere
+        big = torch.zeros(n, h * (d + 3) + 1, device="cuda", dtype=t.dtype)[:, 1:].unflatten(1, (h, d + 3))
+    big[:, :h, :d] = t
+    return big[:, :h, :d]
+
+
+@pytest.mark.parametrize("how", ["heads first", "wide", "odd"])
+@pytest.mark.parametrize("heads, kv_heads, dim", [(4, 2, 64), (6, 2, 72), (2, 1, 40), (8, 2, 128), (64, 1, 64)])
+@pytest.mark.parametrize("ql, kl", [([300, 7, 256], [300, 7, 256]), ([1, 1, 1], [300, 7, 2000]), ([9, 40], [3000, 40])])
+def test_attention_layouts(ql, kl, heads, kv_heads, dim, how):
+    """Queries, keys and values head by head or inside wider rows, outputs in those layouts and at odd elements: the same
+    bits as dense, and nothing written beside them."""
+    import torch
+    from flow_matching_dit_b200 import attention
+    g = gen(heads + dim)
+    q, k, v = (rnd(g, n, h, dim, dtype=torch.bfloat16) for n, h in ((sum(ql), heads), (sum(kl), kv_heads), (sum(kl), kv_heads)))
+    cu = lambda n: torch.tensor([sum(n[:i]) for i in range(len(n) + 1)], dtype=torch.int32, device="cuda")  # noqa: E731
+    args, kw = (cu(ql), cu(kl)), dict(max_q=max(ql), max_k=max(kl), return_lse=True)
+    want, lse = attention(q, k, v, *args, **kw)
+    ref, tol, rl, tl = attention64(q, k, v, ql, kl, [sum(kl[:i]) for i in range(len(kl))], True, dim ** -0.5)
+    within(want, ref, tol, "out")
+    if how != "odd":
+        got, l2 = attention(*(spread(t, how) for t in (q, k, v)), *args, **kw)
+        assert torch.equal(got, want) and torch.equal(l2, lse)
+    out = spread(torch.full_like(want, 9.0), how)
+    base = out._base if out._base is not None else out
+    count = int((base == 9.0).sum())
+    got, l2 = attention(q, k, v, *args, out=out, **kw)
+    assert got is out and torch.equal(out, want) and torch.equal(l2, lse)
+    out.fill_(9.0)
+    assert int((base == 9.0).sum()) == count and int((base != 0).sum()) == count   # zeros beside it, as before
+    clean()
+
+
+@pytest.mark.parametrize("batch", [4000, 65535])
+def test_attention_as_many_sequences_as_there_may_be(batch):
+    """One token over no, one or two keys in each of very many sequences, and prompts as short."""
+    import torch
+    from flow_matching_dit_b200 import attention
+    g = gen(batch)
+    heads, dim = 2, 64
+    nk = torch.arange(batch, device="cuda") % 3
+    ck = torch.cat([nk.new_zeros(1), nk.cumsum(0)])
+    k, v = (rnd(g, int(ck[-1]), 1, dim, dtype=torch.bfloat16) for _ in range(2))
+    for nq in (torch.ones_like(nk), nk):
+        cq = torch.cat([nq.new_zeros(1), nq.cumsum(0)])
+        q = rnd(g, int(cq[-1]), heads, dim, dtype=torch.bfloat16)
+        got, lse = attention(q, k, v, cq.int(), ck.int(), max_q=int(nq.max()), max_k=2, causal=False, return_lse=True)
+        seq = torch.repeat_interleave(torch.arange(batch, device="cuda"), nq)
+        at = (ck[seq][:, None] + torch.arange(2, device="cuda")).clamp_max(k.shape[0] - 1)
+        seen = torch.arange(2, device="cuda") < nk[seq][:, None]
+        sc = torch.einsum("thd,tjd->thj", q.double(), k[at][:, :, 0].double()) * dim ** -0.5
+        # roundings as in the other tests: scores, exponentials, probabilities in bf16 and the output's own
+        e = (dim / 16 + 16) * 2.0 ** -23 * dim ** -0.5 * torch.einsum("thd,tjd->thj", q.double().abs(), k[at][:, :, 0].double().abs()).amax(-1)
+        sc = sc.masked_fill(~seen[:, None], -math.inf)
+        rl = torch.logsumexp(sc, -1)
+        p = torch.exp(sc - rl.clamp_min(-1e300)[..., None])
+        vv = v[at][:, :, 0].double()
+        ref, mag = torch.einsum("thj,tjd->thd", p, vv), torch.einsum("thj,tjd->thd", p, vv.abs())
+        t = mag * (U16 + 2.0 ** -16 + 2 * e[..., None])
+        within(got, ref, t + U16 * (ref.abs() + t) + 1e-30, "out")
+        within(lse, rl, e + 2.0 ** -16 + 2.0 ** -22 * rl.abs().nan_to_num(posinf=0) + 1e-30, "lse")
+    clean()
+
+
+def test_attention_queries_past_31_bits():
+    """Queries and outputs of more than 2^31 elements: the last sequences."""
+    import torch
+    from flow_matching_dit_b200 import attention
+    heads, kv_heads, dim, n, batch = 32, 8, 128, 700, 760
+    g = gen(1)
+    q = torch.empty(n * batch, heads, dim, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    k, v = (torch.empty(n * batch, kv_heads, dim, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    assert q.numel() > 2 ** 31
+    cu = torch.arange(0, n * (batch + 1), n, dtype=torch.int32, device="cuda")
+    out, lse = attention(q, k, v, cu, cu, max_q=n, max_k=n, return_lse=True)
+    for b in (0, batch - 1):
+        rows = slice(b * n, (b + 1) * n)
+        ref, tol, rl, tl = attention64(q[rows], k[rows], v[rows], [n], [n], [0], True, dim ** -0.5)
+        within(out[rows], ref, tol, f"sequence {b}")
+        within(lse[rows], rl, tl, f"lse {b}")
+    clean()
+
+
+def test_attention_sequences_that_begin_late_or_are_all_empty():
+    """Rows in front of the first sequence and behind the last one are left as they were; so are all where no sequence has a
+    query."""
+    import torch
+    from flow_matching_dit_b200 import attention
+    g = gen(2)
+    cu = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for nq in (1, 60):
+        q, k, v = (rnd(g, n, h, 64, dtype=torch.bfloat16) for n, h in ((2 * nq + 9, 4), (500, 2), (500, 2)))
+        out = torch.full_like(q, 7.0)
+        attention(q, k, v, cu(5, 5 + nq, 5 + 2 * nq), cu(100, 230, 499), max_q=nq, max_k=269, out=out)
+        ref, tol, _, _ = attention64(q[5:5 + 2 * nq], k, v, [nq, nq], [130, 269], [100, 230], True, 0.125)
+        within(out[5:5 + 2 * nq], ref, tol, "out")
+        assert (out[:5] == 7).all() and (out[5 + 2 * nq:] == 7).all()
+        out.fill_(7.0)
+        attention(q, k, v, cu(0, 0, 0), cu(0, 20, 500), max_q=0, max_k=480, out=out)
+        attention(q, k, v, cu(3, 3, 3), cu(0, 20, 500), max_q=nq, max_k=480, out=out)
+        assert (out == 7).all()
+    clean()
+
+
 # ---------------------------------------------------------------------------------------------- streams
 
 def test_outputs_belong_to_the_stream_given():
@@ -269,6 +396,72 @@ def test_outputs_belong_to_the_stream_given():
         assert not theirs & {t.data_ptr() for t in [torch.empty_like(t) for t in want for _ in range(8)]}
         with torch.cuda.stream(st):
             assert theirs & {t.data_ptr() for t in [torch.empty_like(t) for t in want]}
+
+
+def test_calls_from_several_host_threads():
+    """Threads with a stream each run the three operators at the same time, errors among the calls."""
+    import threading
+
+    import torch
+    from flow_matching_dit_b200 import GditError, attention, linear, norm_residual
+    bf, made, errors = torch.bfloat16, [], []
+    for i in range(4):
+        g = gen(30 + i)
+        n = 40 * i + 1
+        made.append((rnd(g, n, 512), rnd(g, 512, 512, std=0.05, dtype=bf), rnd(g, 512),
+                     torch.tensor([0, n], dtype=torch.int32, device="cuda"), n))
+
+    def block(h, w, gain, cu, n):
+        h, u = norm_residual(h, None, pre="rms", pre_gain=gain, u_dtype=bf)
+        q = linear(u, w, activation="silu").view(n, 4, 128)
+        return linear(attention(q, q, q, cu, cu, max_q=n, max_k=n).view(n, 512), w, residual=h, out_dtype=torch.float32)
+
+    want = [block(*m) for m in made]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(60):
+                    got = block(*made[i])
+                    with pytest.raises(GditError, match="multiple of 8"):
+                        linear(made[i][1][:, :60], made[i][1][:, :60])
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(got, want[i])
+        except BaseException as e:   # noqa: B902
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(made))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    clean()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_block_that_the_readme_shows(dtype):
+    """Its lines as they stand, on a residual stream of either type."""
+    import os
+    import re
+
+    import torch
+    from flow_matching_dit_b200.build import ROOT
+    text = open(os.path.join(ROOT, "README.md")).read()
+    code = next(c for c in re.findall(r"```python\n(.*?)```", text, re.S) if "norm_residual" in c)
+    g = gen(17)
+    width, heads, kv_heads, dim, tokens, longest = 256, 4, 2, 64, 90, 60
+    bf = torch.bfloat16
+    mat = lambda n, k: rnd(g, n, k, std=k ** -0.5, dtype=bf)  # noqa: E731
+    x = rnd(g, tokens, width, dtype={"f32": torch.float32, "bf16": bf}[dtype])
+    names = dict(torch=torch, x=x, tokens=tokens, heads=heads, kv_heads=kv_heads, dim=dim, longest=longest,
+                 cu=torch.tensor([0, 30, 90], dtype=torch.int32, device="cuda"), w_qkv=mat((heads + 2 * kv_heads) * dim, width),
+                 b_qkv=rnd(g, (heads + 2 * kv_heads) * dim), w_o=mat(width, heads * dim), w_1=mat(4 * width, width),
+                 w_2=mat(width, 4 * width), gate=rnd(g, width), **{f"g{i}": rnd(g, width, std=0.1) + 1 for i in (1, 2, 3)})
+    exec(code, names)
+    h = names["h"]
+    assert h.dtype == x.dtype and h.shape == x.shape and torch.isfinite(h).all() and not torch.equal(h, x)
 
 
 # ---------------------------------------------------------------------------------------------- autograd
