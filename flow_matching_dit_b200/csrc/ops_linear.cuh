@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (lane == 0) bulk_wait<0>();
   }
   __syncthreads();
+  if (threadIdx.x == 0) op_leave(&s_abort);
+  __syncwarp();
   cluster_sync();   // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc_fence_after();

@@ -24,3 +24,14 @@ def test_a_warp_has_converged_before_a_lane_arrives_for_it(name):
             found += 1
             assert lines[i - 1] == "__syncwarp();", "\n".join(lines[i - 3:i + 1])
     assert found >= 1
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_kernels_that_wait_leave_after_their_copies(name):
+    """A bounded wait that has run out lets a kernel's loops run to their end with copies into shared memory under way:
+    each kernel whose waits are bounded gives them time to land before its CTAs leave."""
+    src = open(os.path.join(PKG, "csrc", name)).read()
+    kernels = re.findall(r"__global__ void.*?\n}\n", src, re.S)
+    assert kernels
+    for k in kernels:
+        assert "op_wait" in k and k.count("op_leave(&s_abort)") == 1, k[:200]
