@@ -320,3 +320,8 @@ def debug_wait_expiry(device: int = 0, limit_ns: int = 1_000_000) -> int:
     """Status of one bounded wait on an mbarrier that nothing arrives at
     (gdit_debug_wait_expiry): GDIT_ETIMEOUT is the expected result."""
     return _lib.gdit_debug_wait_expiry(int(device), int(limit_ns))
+
+
+def debug_op_wait_expiry(device: int = 0, limit_ns: int = 1_000_000) -> int:
+    """The same of the operators' waits (gdit_debug_op_wait_expiry)."""
+    return _lib.gdit_debug_op_wait_expiry(int(device), int(limit_ns))

@@ -115,6 +115,7 @@ _SIGS = {
     "gdit_norm_residual": (_I, [ctypes.POINTER(gdit_norm_args), _P]),
     "gdit_attention": (_I, [ctypes.POINTER(gdit_attention_args), _P]),
     "gdit_op_status": (_I, [_I, _P]),
+    "gdit_debug_op_wait_expiry": (_I, [_I, ctypes.c_ulonglong]),
 }
 
 _lock = threading.Lock()
@@ -263,3 +264,7 @@ def gdit_debug_linear_plan(*a):
 
 def gdit_op_status(device, stream):
     return lib().gdit_op_status(device, stream)
+
+
+def gdit_debug_op_wait_expiry(device, limit_ns):
+    return lib().gdit_debug_op_wait_expiry(device, limit_ns)

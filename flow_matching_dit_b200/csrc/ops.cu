@@ -53,6 +53,16 @@ int current_sms() {
   return sms[dev];
 }
 
+// A device made current, and the one before again at the end.
+struct DeviceGuard {
+  int before = 0;
+  explicit DeviceGuard(int device) {
+    CUDA_TRY(cudaGetDevice(&before));
+    CUDA_TRY(cudaSetDevice(device));
+  }
+  ~DeviceGuard() { cudaSetDevice(before); }
+};
+
 bool is_dtype(int t) { return t == GDIT_F32 || t == GDIT_BF16; }
 int size_of(int t) { return t == GDIT_F32 ? 4 : 2; }
 bool aligned_to(const void* p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes) == 0; }
@@ -93,6 +103,25 @@ bool linear_args(const gdit_linear_args* p, LinearArgs& a) {
 }
 
 __global__ void clear_status_kernel(unsigned bits) { atomicAnd(&g_op_status, ~bits); }
+
+// Two warps and the operators' three waits on a barrier that nothing arrives at: the
+// first runs out, the others end with it.
+__global__ void op_wait_expiry_kernel(unsigned long long limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ volatile int s_abort;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) op_wait(&bar, 0, &s_abort, limit_ns);
+  __syncwarp();
+  op_wait_through(&bar, 0, &s_abort);
+  op_wait_warp_cluster(&bar, 0, &s_abort);
+  __syncthreads();
+  if (threadIdx.x == 0) op_leave(&s_abort);
+}
 
 }  // namespace
 
@@ -218,18 +247,13 @@ int gdit_attention(const gdit_attention_args* p, void* cuda_stream) {
 int gdit_op_status(int device, void* cuda_stream) {
   unsigned bits = 0;
   const int rc = guarded_op([&] {
-    int before = 0, n = 0;
+    int n = 0;
     if (cudaGetDeviceCount(&n) != cudaSuccess || n == 0) {
       cudaGetLastError();
       throw GditError(GDIT_ENODEV, "no CUDA device");
     }
     REQUIRE(device >= 0 && device < n, "device %d out of range", device);
-    CUDA_TRY(cudaGetDevice(&before));
-    struct Restore {
-      int d;
-      ~Restore() { cudaSetDevice(d); }
-    } restore{before};
-    CUDA_TRY(cudaSetDevice(device));
+    const DeviceGuard guard(device);
     cudaStream_t s = (cudaStream_t)cuda_stream;
     CUDA_TRY(cudaMemcpyFromSymbolAsync(&bits, g_op_status, sizeof(bits), 0, cudaMemcpyDeviceToHost, s));
     CUDA_TRY(cudaStreamSynchronize(s));
@@ -245,6 +269,22 @@ int gdit_op_status(int device, void* cuda_stream) {
       throw GditError(GDIT_EDEVICE, "attention: sequence offsets or lengths out of range (those sequences are skipped)");
   });
   return rc;
+}
+
+int gdit_debug_op_wait_expiry(int device, unsigned long long limit_ns) {
+  const int rc = guarded_op([&] {
+    REQUIRE(limit_ns >= 1000ull && limit_ns <= 1000000000ull, "limit_ns %llu outside [1 us, 1 s]", limit_ns);
+    int n = 0;
+    if (cudaGetDeviceCount(&n) != cudaSuccess || n == 0) {
+      cudaGetLastError();
+      throw GditError(GDIT_ENODEV, "no CUDA device");
+    }
+    REQUIRE(device >= 0 && device < n, "device %d of %d", device, n);
+    const DeviceGuard guard(device);
+    op_wait_expiry_kernel<<<1, 64>>>(limit_ns);
+    CUDA_TRY(cudaGetLastError());
+  });
+  return rc != GDIT_OK ? rc : gdit_op_status(device, nullptr);
 }
 
 }  // extern "C"

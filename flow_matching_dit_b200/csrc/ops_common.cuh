@@ -46,12 +46,13 @@ __device__ __forceinline__ uint2 load_b16x4(const __nv_bfloat16* p) {
 // Waits for a phase of an mbarrier of this CTA; false once a wait of the CTA has
 // run out (2 s), which the status word then says.  *abort is in shared memory:
 // the CTA's other waits give up soon after, other calls are not concerned.
-__device__ __forceinline__ bool op_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool op_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                        unsigned long long limit_ns = kWaitTimeoutNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
   while (!*abort) {
     if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
-    if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+    if (globaltimer_ns() - t0 > limit_ns) {
       *abort = 1;
       atomicOr(&g_op_status, DEV_ERR_TIMEOUT);
     }

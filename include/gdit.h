@@ -514,6 +514,14 @@ int gdit_attention(const gdit_attention_args* a, void* cuda_stream);
  * Clears it.  One status word per device, shared by all streams. */
 int gdit_op_status(int device, void* cuda_stream);
 
+/* Failure detection check, like gdit_debug_wait_expiry, of the operators' own
+ * waits: a kernel on `device` waits, in each of their forms, on an mbarrier
+ * that nothing ever arrives at, with a limit of limit_ns nanoseconds (1 us to
+ * 1 s).  No GPU fault or hang.  Returns what gdit_op_status then says:
+ * GDIT_ETIMEOUT is the expected outcome; GDIT_EINVAL for a bad limit or
+ * device, GDIT_ENODEV without a GPU.  Synchronous. */
+int gdit_debug_op_wait_expiry(int device, unsigned long long limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

@@ -516,3 +516,24 @@ def test_writes_into_given_tensors_are_seen_by_autograd():
         with torch.inference_mode():
             call(torch.ones(shape, device="cuda", dtype=dtype))   # such tensors have no version
     clean()
+
+
+# ---------------------------------------------------------------------------------------------- waits
+
+@pytest.mark.parametrize("limit_ns", [1000, 20_000_000])
+def test_a_wait_that_runs_out_is_reported_and_calls_go_on(limit_ns):
+    """The operators' waits on a barrier that nothing arrives at: the first ends after its limit, the others with it (their
+    own would be 2 s), and the status says so once."""
+    import time
+
+    import torch
+    from flow_matching_dit_b200 import _lib, debug_op_wait_expiry, linear, op_status
+    x = rnd(gen(3), 64, 256, dtype=torch.bfloat16)
+    want = linear(x, x)
+    clean()
+    t = time.perf_counter()
+    assert debug_op_wait_expiry(0, limit_ns) == _lib.GDIT_ETIMEOUT
+    assert limit_ns * 1e-9 <= time.perf_counter() - t < 1.0
+    assert op_status() == 0
+    assert torch.equal(linear(x, x), want)
+    clean()
