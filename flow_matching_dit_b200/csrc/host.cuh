@@ -53,16 +53,16 @@ typedef CUresult (*PFN_encodeTiled_t)(CUtensorMap*, CUtensorMapDataType, cuuint3
                                        const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                        CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// Looked up once, by whichever thread comes first (again after a failure).
 inline PFN_encodeTiled_t encode_fn() {
-  static PFN_encodeTiled_t fn = nullptr;
-  if (fn == nullptr) {
+  static const PFN_encodeTiled_t fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     CUDA_TRY(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q));
     if (p == nullptr || q != cudaDriverEntryPointSuccess)
       throw GditError(GDIT_ECUDA, "cuTensorMapEncodeTiled not available from the driver");
-    fn = reinterpret_cast<PFN_encodeTiled_t>(p);
-  }
+    return reinterpret_cast<PFN_encodeTiled_t>(p);
+  }();
   return fn;
 }
 

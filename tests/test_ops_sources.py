@@ -35,3 +35,12 @@ def test_kernels_that_wait_leave_after_their_copies(name):
     assert kernels
     for k in kernels:
         assert "op_wait" in k and k.count("op_leave(&s_abort)") == 1, k[:200]
+
+
+def test_no_plain_static_is_written_after_it_was_made():
+    """Calls run in several host threads at once: what the operators' host code keeps is const, atomic, behind a mutex or a
+    thread's own."""
+    for name in ("host.cuh", "ops.cu", "ops_common.cuh", "ops_linear.cuh", "ops_norm.cuh", "ops_attention.cuh"):
+        for line in open(os.path.join(PKG, "csrc", name)).read().split("\n"):
+            if re.match(r"\s+static (?!constexpr|const |__device__|_?_?inline)", line):
+                assert re.search(r"std::(mutex|atomic|map|set)|int sms\[kMaxDevices\]", line), line   # (the last three under a mutex)
