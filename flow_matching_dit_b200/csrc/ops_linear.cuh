@@ -286,6 +286,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int cols = a.out_f32 ? 32 : 64, chunks = BN / cols / 2;   // columns of a box, boxes of this warp in a tile
     const int sw = lane & 7;
     const bool res = a.residual != nullptr, res_tma = res && a.tma;
+    // TMA clips a store at the matrix' last column in units of 16 bytes: where that lies inside a unit, it would write
+    // what is beside the output, and the box over the last column is written by words
+    const bool ragged = (a.n & (a.out_f32 ? 3 : 7)) != 0;
     int it = 0, seq = 0;
     for (int t = cid; t < total; t += ncl, ++it) {
       lin_pair_tile(t, mt, nt, mi, ni);
@@ -374,18 +377,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
           }
         }
-        if (!a.tma) {
+        const bool words = !a.tma || (ragged && n < a.n && n + cols > a.n);
+        if (words) {
           __syncwarp();
           if (ym < a.m) box_to(box, a.out, a.ldo, a.out_f32, ym, a.m, n, a.n);
           __syncwarp();
-          if (res && ym < a.m && c + 2 < chunks) gather(seq + 2, n + 4 * cols);
-          continue;
+          if (!a.tma) {
+            if (res && ym < a.m && c + 2 < chunks) gather(seq + 2, n + 4 * cols);
+            continue;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (n < a.n && ym < a.m) tma_store_2d(&tmO, box, n, ym);   // clipped at the matrix' edges
-          bulk_commit();
+          if (!words && n < a.n && ym < a.m) tma_store_2d(&tmO, box, n, ym);   // clipped at the matrix' edges
+          bulk_commit();   // (a group a box, also without a store: the boxes are counted by them)
         }
       }
     }

@@ -110,6 +110,29 @@ def test_linear_pair_strided_and_in_place(m, n, k, bn, out, offset, pad):
     clean()
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("less", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("m, n, k, bn", [(4100, 4104, 2048, 256), (4100, 1032, 520, 128)])
+def test_linear_pair_last_column_inside_16_bytes(m, n, k, bn, out, less):
+    """Rows that TMA can address, of which the output takes a width that is no multiple of 16 bytes: nothing beside it is
+    written, with a residual, without and in place."""
+    import torch
+    from flow_matching_dit_b200 import linear
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    g = gen(n + less)
+    full, n = n, n - less
+    on_pairs(m, n, k, bn, dt, True, True)
+    x, w, b = rnd(g, m, k, dtype=torch.bfloat16), rnd(g, n, k, std=k ** -0.5, dtype=torch.bfloat16), rnd(g, n)
+    wide = rnd(g, m, full + 8, dtype=dt)
+    before, view = wide.clone(), wide[:, :n]
+    for residual in (None, rnd(g, m, full + 8, dtype=dt)[:, :n], view):
+        ref, tol = linear64(x, w, b, "relu", None if residual is None else residual.clone(), dt)
+        linear(x, w, b, activation="relu", residual=residual, out=view)
+        within(view, ref, tol)
+        assert torch.equal(wide[:, n:], before[:, n:])
+    clean()
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_linear_pair_activations_far_out(act, out):
