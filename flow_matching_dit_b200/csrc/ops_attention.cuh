@@ -136,7 +136,9 @@ struct AttnTile {
 
 // Walks tiles in an order that all warps and CTAs agree on: all lanes of a warp
 // together.  A group of 32 sequences at a time, one a lane; within a group by
-// falling position (the longest tiles of causal prompts first).
+// falling position (the longest tiles of causal prompts first).  Every warp reads every
+// group's offsets for itself, so that a CTA's time grows with the batch, also where its
+// own tiles are few.
 struct TileWalk {
   int base;              // first sequence of the group
   long long before;      // tiles in front of the group

@@ -202,8 +202,9 @@ struct RowTeam {
 constexpr int kNormThreads = 512;   // most threads of a row's team
 
 // THREADS: most of a CTA, 256 or, for rows that need a wider team, 512.  As many CTAs an
-// SM as the registers of h, y and their addresses allow without spilling (2, 3 or 4): with
-// all the registers the compiler likes, 2999 x 1337 took 24 us instead of 20.
+// SM as the registers of h, y and their addresses allow (2, 3 or 4; of all forms only the one
+// value by value with 24 a thread spills, 8 bytes): with all the registers the compiler
+// likes, 2999 x 1337 took 24 us instead of 20.
 template <RowLayout LAYOUT, int NU, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NU == 8 ? 2 : NU == 6 ? 3 : 4) norm_kernel(const NormArgs a, int warps, int teams) {
   __shared__ float red[kNormThreads / 32 * 2];
@@ -270,7 +271,9 @@ inline void launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
   const int width = a.dim + (units ? shift : 0);   // with what the shift may add in front
   // Warps of a row: as few as hold it with 32 values a thread, so that a row of
   // up to 1024 needs no barrier; more where the rows would leave an SM fewer than 32
-  // (4352 x 1024: 14 us in two warps a row, 20 in one, 19 in four).
+  // (4352 x 1024: 14 us in two warps a row, 20 in one, 19 in four).  Above 8 warps a thread
+  // holds 32 values all the same: where 3, 5, 6 or 7 warps were doubled past 8, those that
+  // the row does not need only join the barriers.
   int warps = (width + 1023) / 1024;
   while (a.rows * warps < 32ll * sms && 128 * warps < width && warps < 8) warps *= 2;
   const int per = (width + 128 * warps - 1) / (128 * warps);   // units of 4 values a thread

@@ -58,7 +58,8 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out=None, out_d
 
     bias: float32 [n].  activation: "none", "relu", "gelu" (erf), "gelu_tanh" or "silu".  residual and the result are
     [m, n] of out_dtype (float32 or bfloat16; default: out's, else residual's, else bfloat16).  out may be the
-    residual: the sum is then added in place.  The rows of x, w, residual and out may be strided."""
+    residual: the sum is then added in place.  It may not overlap x or w.  The rows of x, w, residual and out may be
+    strided."""
     return _call_linear(x, w, bias, activation, residual, out, out_dtype, stream)
 
 
@@ -75,7 +76,7 @@ def norm_residual(h, y=None, *, post=None, post_gain=None, post_bias=None, gate=
     h and y are float32 or bfloat16; h' has h's type, u has u_dtype (default: out_u's, else y's, else bfloat16).
     Without y the branch is left out, and h' is h itself when residual_scale is 1.  u is None when there is nothing
     to compute for it (no pre, scale or shift, and neither out_u nor u_dtype).  out_h may be h, for an update in
-    place."""
+    place, and out_u may be y."""
     return _call_norm_residual(h, y, post, post_gain, post_bias, gate, residual_scale, pre, pre_gain, pre_bias, scale,
                                shift, row_group, eps, out_h, out_u, u_dtype, stream)
 
@@ -88,7 +89,8 @@ def attention(q, k, v, cu_q, cu_k, *, max_q, max_k, causal=True, scale=None, k_l
     with k_len (int32 [batch]), the first k_len[b] keys of that range: a slot of a cache.  causal: the last query of a
     sequence sees all its keys, the one before it all but the last, and so on, which serves whole prompts, further
     pieces of prompts and single tokens over a cache.  max_q and max_k bound the sequences' lengths.  heads is a
-    multiple of kv_heads; head_dim a multiple of 8 up to 128; q, k and v may be slices of one tensor.
+    multiple of kv_heads; head_dim a multiple of 8 up to 128; q, k and v may be slices of one tensor, and out may be q,
+    but not overlap k or v.
 
     Returns the output [total_q, heads, head_dim], or (output, lse) with return_lse: lse float32 [total_q, heads].
     A query without keys gives 0 and -inf.  Rows behind the last sequence are not written."""

@@ -366,7 +366,10 @@ int gdit_gemm_static_scratch(const void* A, const void* B, const float* bias, fl
  *   - Sums, softmax statistics and norms are f32; outputs are rounded once,
  *     to nearest even.  Sums of products run on the tensor cores, whose
  *     accumulation cuts bits off: k products lose about 1.3e-9 k of the result
- *     (1e-5 at k = 8192, which only an f32 output shows).
+ *     (1e-5 at k = 8192, which only an f32 output shows).  gdit_attention
+ *     multiplies the values with probabilities rounded to bf16, each off by at
+ *     most 2^-8 of itself; what they are divided by, and lse, is the sum of the
+ *     unrounded ones.
  *   - Results are the same bit for bit from call to call on the same inputs.
  *   - What the host cannot see is checked on the device: a row_group entry out
  *     of range, sequence offsets that decrease, end past the tensor or exceed
@@ -383,6 +386,7 @@ int gdit_gemm_static_scratch(const void* A, const void* B, const float* bias, fl
 #define GDIT_ACT_RELU 1
 #define GDIT_ACT_GELU 2         /* by the normal distribution: v * Phi(v); good to 2^-19 of the result for v >= -1,
                                    2^-16 down to -5, 2^-14 to -7, 2^-10 to -12.9, 0 below */
+/* (these two: v times a factor in (0, 1), which is 0 from 2^-62 down) */
 #define GDIT_ACT_GELU_TANH 3    /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
 #define GDIT_ACT_SILU 4         /* v / (1 + exp(-v)) */
 
@@ -438,8 +442,10 @@ int gdit_debug_linear_plan(const gdit_linear_args* a, int num_sms, int* pair, in
  *   scale, shift  f32 [mod_groups, dim], NULL = 0
  *   row_group int32 [rows]: the group of each row, needed when gate_groups or
  *             mod_groups is above 1; a tensor of one group serves every row
- * dim in [1, 16384]; strides >= dim; pointers aligned to their element
- * (16-byte aligned rows of a multiple of 8 elements run fastest). */
+ * dim in [1, 16384]; strides >= dim; pointers aligned to their element.  Rows
+ * go by units of 4 elements: fastest are widths and strides of whole units with
+ * f32 tensors aligned to 16 bytes and bf16 ones to 8; strides that are not, but
+ * alike in all matrices up to whole units, come next. */
 typedef struct {
   const void* h;
   const void* y;
